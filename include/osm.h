@@ -414,6 +414,109 @@ OSM_API int osm_ffn_block_host(const osm_plan* up, const osm_plan* down, const u
                                const float* bias_down, uint16_t* Y_host, void* workspace, size_t workspace_bytes,
                                void* stream);
 
+/* ---- around the block: norms, gate and residual ----------------------------
+ * What stands between a transformer block's layers: the norm in front of a
+ * sublayer with its modulation, and the gated sum onto the residual stream
+ * behind it. (The paper smooths and quantises the FFN's linear maps and
+ * leaves these in high precision; they produce the activations that
+ * osm_quantize_act takes and consume what the down-projection gives.) */
+
+/* type of a residual stream: R, X and the outputs that continue it */
+#define OSM_DT_BF16 0
+#define OSM_DT_F32  1
+
+/* N(x) = (x - mean) / sqrt(var + eps), var = mean((x - mean)^2) over the row,
+ * or x / sqrt(mean(x^2) + eps). Statistics are FP32, the variance formed from
+ * deviations (never as a difference of sums). */
+#define OSM_NORM_LAYER 0
+#define OSM_NORM_RMS   1
+
+/* A norm with its affine part and its modulation:
+ *   norm(x) = (N(x) * weight + bias) * (1 + scale) + shift     (FP32)
+ * weight, bias: device float[D] or NULL (1 and 0). scale, shift: device rows
+ * of D floats, mod_stride floats apart (so that they may be slices of one
+ * embedding), or NULL (0); token t takes row t / mod_rows (mod_rows >= M: one
+ * row for all; tokens per sample: one row per sample; 1: one row per token).
+ * eps is finite and > 0; pointers 16-byte aligned, mod_stride % 4 == 0 (and
+ * >= D where there are several rows). mod_rows and mod_stride are not read
+ * without scale and shift. The struct itself is host memory, read during the
+ * call. */
+typedef struct {
+    int32_t kind; /* OSM_NORM_* */
+    float eps;
+    const float* weight;
+    const float* bias;
+    const float* scale;
+    const float* shift;
+    int64_t mod_rows;
+    int64_t mod_stride;
+} osm_norm_spec;
+
+/* H[t] = bf16(norm(X[t])): X [M][D] BF16 or FP32 (x_dtype), H [M][D] BF16 --
+ * the input of osm_quantize_act, osm_act_amax_accumulate or osm_linear_hp.
+ * 1 <= M < 2^31, 8 <= D <= 65536, D % 8 == 0. H may be X (BF16). */
+OSM_API int osm_norm_modulate(const void* X, int x_dtype, int64_t M, int64_t D, const osm_norm_spec* norm,
+                              uint16_t* H, void* stream);
+
+/* The step from one sublayer to the next:
+ *   R_out[t] = T(R[t] + alpha * gate[t / gate_rows] * post(Y[t])),
+ *   H[t]     = bf16(pre(R_out[t]))     (of the rounded R_out)
+ * R, R_out [M][D] of type T (r_dtype), Y, H [M][D] BF16. post: the norm
+ * behind the sublayer, or NULL (Y itself; scale and shift of `post` must be
+ * NULL). gate: device rows of D floats, gate_stride floats apart, or NULL (1);
+ * gate_rows and gate_stride as mod_rows and mod_stride. pre: the next
+ * sublayer's norm, or NULL (then H is NULL). R_out may be R, H may be Y. */
+OSM_API int osm_residual_norm(const void* R, int r_dtype, const uint16_t* Y, int64_t M, int64_t D,
+                              const osm_norm_spec* post, const float* gate, int64_t gate_rows, int64_t gate_stride,
+                              float alpha, const osm_norm_spec* pre, void* R_out, uint16_t* H, void* stream);
+
+/* osm_norm_modulate followed by osm_quantize_act in one pass: writes the
+ * same packed operands (bit for bit), without H in memory. X [M][plan->K]. */
+OSM_API int osm_norm_quantize_act(const osm_plan* plan, const void* X, int x_dtype, int64_t M,
+                                  const osm_norm_spec* norm, uint8_t* a_codes, uint8_t* a_scales, uint16_t* a_hp,
+                                  void* stream);
+
+/* osm_dual_gemm onto the residual stream, in its epilogue:
+ *   Y = T(R + gate[t / gate_rows] * (acc + bias))
+ * with acc as osm_dual_gemm defines it (both formats), R and Y [M][N] of type
+ * T (r_dtype), bias float[N] or NULL, gate rows of N floats as in
+ * osm_residual_norm, or NULL. The product is gated and added in FP32 and
+ * rounded once. Y may be R. */
+OSM_API int osm_dual_gemm_residual(const osm_plan* plan, const uint8_t* a_codes, const uint8_t* a_scales,
+                                   const uint16_t* a_hp, int64_t M, const uint8_t* w_codes, const uint8_t* w_scales,
+                                   const uint16_t* w_hp, const float* bias, const float* gate, int64_t gate_rows,
+                                   int64_t gate_stride, const void* R, int r_dtype, void* Y, void* stream);
+
+/* ---- layers kept in high precision ------------------------------------------
+ * A deployment keeps some layers out of the 4-bit path. A plan with k = K and
+ * s = 1 stands for such a layer: osm_pack_weights gives its transposed BF16
+ * weights w_hp [N][kp], and osm_linear_hp runs the product from X itself:
+ *   y = act(X W + bias),  Y = T([R +] [gate[t / gate_rows] *] y)
+ * X [M][K] BF16; FP32 accumulation; act one of OSM_ACT_*; bias float[N] or
+ * NULL; gate as above or NULL; R [M][N] of Y's type T (y_dtype) or NULL. Y
+ * may be R. 1 <= M < 2^31. The plan's outlier branch must be BF16. A pipeline
+ * wait that exceeds the plan's wait limit sets OSM_STATUS_TIMEOUT. */
+#define OSM_ACT_NONE 0
+#define OSM_ACT_GELU 1 /* the tanh form of the FFN epilogues */
+#define OSM_ACT_SILU 2 /* x / (1 + exp(-x)) */
+OSM_API int osm_linear_hp(const osm_plan* plan, const uint16_t* X, int64_t M, const uint16_t* w_hp, const float* bias,
+                          int act, const float* gate, int64_t gate_rows, int64_t gate_stride, const void* R, void* Y,
+                          int y_dtype, void* stream);
+
+/* ---- one FFN sublayer ---------------------------------------------------------
+ *   R_out = T(R + gate * (FFN(pre(R)) + bias_down))
+ * osm_norm_quantize_act(up), osm_dual_gemm(up, OSM_EPI_GELU_REQUANT, down) and
+ * osm_dual_gemm_residual(down), with the weights and the workspace of
+ * osm_ffn_block (osm_ffn_workspace_size). R, R_out [M][up->K] of type r_dtype,
+ * down->N == up->K; both plans MXFP4. R_out may be R. Returns the first
+ * failing call's error; a failure of the second or third call leaves the
+ * earlier work enqueued. */
+OSM_API int osm_ffn_sublayer(const osm_plan* up, const osm_plan* down, const osm_norm_spec* pre, const void* R,
+                             int r_dtype, int64_t M, const uint8_t* wu_codes, const uint8_t* wu_scales,
+                             const uint16_t* wu_hp, const uint8_t* wd_codes, const uint8_t* wd_scales,
+                             const uint16_t* wd_hp, const float* bias_down, const float* gate, int64_t gate_rows,
+                             int64_t gate_stride, void* R_out, void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---- allocation-free device forward --------------------------------------
  * The paper has no counterpart to this entry point; it serves callers that
  * build their plans and pack their weights at load time but cannot

@@ -31,6 +31,9 @@ STATUS_NONFINITE = 2
 DEBUG_STARVE_QUANTIZE = 1
 WSCALE_1x32, WSCALE_TILE32x32, WSCALE_STRIP128x1 = 0, 1, 2
 EPI_F32, EPI_BF16, EPI_GELU_REQUANT, EPI_GELU_BF16 = 0, 1, 2, 3
+DT_BF16, DT_F32 = 0, 1
+NORM_LAYER, NORM_RMS = 0, 1
+ACT_NONE, ACT_GELU, ACT_SILU = 0, 1, 2
 
 # Every entry point declared in include/osm.h, with its ctypes signature.
 _P, _I64, _I, _U64, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_uint64, ctypes.c_size_t
@@ -69,6 +72,12 @@ _SIGNATURES = {
     "osm_ffn_host_workspace_size": (_SZ, [_P, _P, _I64]),
     "osm_ffn_block": (_I, [_P, _P, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "osm_ffn_block_host": (_I, [_P, _P, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "osm_norm_modulate": (_I, [_P, _I, _I64, _I64, _P, _P, _P]),
+    "osm_residual_norm": (_I, [_P, _I, _P, _I64, _I64, _P, _P, _I64, _I64, ctypes.c_float, _P, _P, _P, _P]),
+    "osm_norm_quantize_act": (_I, [_P, _P, _I, _I64, _P, _P, _P, _P, _P]),
+    "osm_dual_gemm_residual": (_I, [_P, _P, _P, _P, _I64, _P, _P, _P, _P, _P, _I64, _I64, _P, _I, _P, _P]),
+    "osm_linear_hp": (_I, [_P, _P, _I64, _P, _P, _I, _P, _I64, _I64, _P, _P, _I, _P]),
+    "osm_ffn_sublayer": (_I, [_P, _P, _P, _P, _I, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _P, _P, _SZ, _P]),
     "osm_last_error": (ctypes.c_char_p, []),
 }
 
@@ -547,6 +556,212 @@ def scales_to_logical(swizzled: np.ndarray, rows: int, nblocks: int) -> np.ndarr
     return out
 
 
+# ----------------------------------------------------------------- around the layers
+
+class _NormSpec(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("eps", ctypes.c_float), ("weight", _P), ("bias", _P), ("scale", _P),
+                ("shift", _P), ("mod_rows", _I64), ("mod_stride", _I64)]
+
+
+def _here(t, name):
+    """`t` has to be on the current device: the kernels are launched there."""
+    import torch
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _operand(t, name, dtypes, shape, allow_none=False):
+    """Device pointer of a contiguous tensor of this shape on the current device."""
+    if t is None and allow_none:
+        return None
+    p = _ptr(t, name, dtypes)
+    _here(t, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, needs {tuple(shape)}")
+    return p
+
+
+def _stream_type(t, name):
+    """DT_* of a residual stream tensor."""
+    import torch
+    if t.dtype == torch.float32:
+        return DT_F32
+    if t.dtype == torch.bfloat16:
+        return DT_BF16
+    raise ValueError(f"{name} has dtype {t.dtype}, expected torch.bfloat16 or torch.float32")
+
+
+def _vector(t, name, D, allow_none=True):
+    import torch
+    return _operand(t, name, (torch.float32,), (D,), allow_none)
+
+
+def _shared_rows(t, name, M, D, rows):
+    """(pointer, rows, stride) of modulation or gate rows: [D] (one row), or [B][D] whose rows may lie apart (a
+    slice of a wider tensor); `rows` tokens share a row (default: M tokens in B equal parts)."""
+    import torch
+    if t is None:
+        return None, 1, 0
+    if t.dim() not in (1, 2) or t.dtype != torch.float32 or not t.is_cuda:
+        raise ValueError(f"{name} must be a float32 CUDA tensor [D] or [B][D]")
+    _here(t, name)
+    B = 1 if t.dim() == 1 else t.shape[0]
+    if t.shape[-1] != D or t.stride(-1) != 1:
+        raise ValueError(f"{name} needs {D} contiguous columns")
+    if rows is None:
+        if B < 1 or M % B:
+            raise ValueError(f"{name} has {B} rows for {M} tokens: say how many tokens share one")
+        rows = M // B
+    if rows < 1 or -(-M // rows) > B:
+        raise ValueError(f"{name} has {B} rows, {M} tokens by {rows} need {-(-M // max(rows, 1))}")
+    return ctypes.c_void_p(t.data_ptr()), int(rows), int(t.stride(0)) if t.dim() == 2 else D
+
+
+class Norm:
+    """A norm (NORM_LAYER or NORM_RMS) with its affine part (weight, bias: [D] float32) and its modulation (scale,
+    shift: [D] or [B][D] float32, `mod_rows` tokens to a row): osm_norm_spec. Holds its tensors."""
+
+    def __init__(self, kind: int = NORM_LAYER, eps: float = 1e-6, weight=None, bias=None, scale=None, shift=None,
+                 mod_rows: int | None = None):
+        self.kind, self.eps, self.weight, self.bias = int(kind), float(eps), weight, bias
+        self.scale, self.shift, self.mod_rows = scale, shift, mod_rows
+
+    def spec(self, M: int, D: int) -> _NormSpec:
+        scale, rows, stride = _shared_rows(self.scale, "scale", M, D, self.mod_rows)
+        shift, rows2, stride2 = _shared_rows(self.shift, "shift", M, D, self.mod_rows)
+        if self.scale is None:
+            rows, stride = rows2, stride2
+        elif self.shift is not None and (rows2 != rows or (rows < M and stride2 != stride)):
+            raise ValueError("scale and shift must have the same rows and row stride")
+        return _NormSpec(self.kind, self.eps, _vector(self.weight, "weight", D), _vector(self.bias, "bias", D), scale,
+                         shift, rows, stride)
+
+
+def _new(shape, dtype, like, stream):
+    """An output tensor, allocated for the stream that will write it."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    s = torch.cuda.ExternalStream(stream, device=like.device) if isinstance(stream, int) else stream
+    with torch.cuda.stream(s):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def norm_modulate(X, norm: Norm, out=None, stream=None):
+    """H = bf16(norm(X)) (osm_norm_modulate). X: [M][D] BF16 or float32; out: [M][D] BF16 (may be X)."""
+    import torch
+    M, D = X.shape
+    dt = _stream_type(X, "X")
+    if out is None:
+        out = _new((M, D), torch.bfloat16, X, stream)
+    _check(lib().osm_norm_modulate(_operand(X, "X", None, (M, D)), dt, M, D, ctypes.byref(norm.spec(M, D)),
+                                   _operand(out, "out", (torch.bfloat16,), (M, D)), _stream(stream)))
+    return out
+
+
+def residual_norm(R, Y, gate=None, gate_rows: int | None = None, alpha: float = 1.0, post: Norm | None = None,
+                  pre: Norm | None = None, out=None, h=None, stream=None):
+    """(R + alpha * gate * post(Y), pre of it in BF16 or None) (osm_residual_norm). R: [M][D] BF16 or float32, Y: [M][D]
+    BF16; out may be R, h may be Y."""
+    import torch
+    M, D = R.shape
+    dt = _stream_type(R, "R")
+    if out is None:
+        out = _new((M, D), R.dtype, R, stream)
+    if pre is None:
+        if h is not None:
+            raise ValueError("h goes with pre")
+    elif h is None:
+        h = _new((M, D), torch.bfloat16, R, stream)
+    g, rows, stride = _shared_rows(gate, "gate", M, D, gate_rows)
+    bf = (torch.bfloat16,)
+    _check(lib().osm_residual_norm(_operand(R, "R", None, (M, D)), dt, _operand(Y, "Y", bf, (M, D)), M, D,
+                                   ctypes.byref(post.spec(M, D)) if post is not None else None, g, rows, stride,
+                                   float(alpha), ctypes.byref(pre.spec(M, D)) if pre is not None else None,
+                                   _operand(out, "out", (R.dtype,), (M, D)),
+                                   _operand(h, "h", bf, (M, D), allow_none=True), _stream(stream)))
+    return out, h
+
+
+def _packed_ptrs(plan: Plan, rows: int, codes, scales, hp, which: str):
+    cb, sb, hb = plan.sizes(rows)
+    for t, n in ((codes, "codes"), (scales, "scales"), (hp, "hp")):
+        if t is not None:
+            _here(t, f"{which}_{n}")
+    return (_ptr(codes, f"{which}_codes", _u8_types(), cb, allow_none=cb == 0),
+            _ptr(scales, f"{which}_scales", _u8_types(), sb, allow_none=sb == 0),
+            _ptr(hp, f"{which}_hp", _bf16_types(), hb, allow_none=hb == 0))
+
+
+def norm_quantize_act(plan: Plan, X, norm: Norm, a_codes, a_scales, a_hp, stream=None):
+    """quantize_act of norm_modulate(X) in one pass (osm_norm_quantize_act). X: [M][plan.K] BF16 or float32."""
+    M = X.shape[0]
+    _check(lib().osm_norm_quantize_act(plan.handle, _operand(X, "X", None, (M, plan.K)), _stream_type(X, "X"), M,
+                                       ctypes.byref(norm.spec(M, plan.K)),
+                                       *_packed_ptrs(plan, M, a_codes, a_scales, a_hp, "a"), _stream(stream)))
+
+
+def dual_gemm_residual(plan: Plan, a_codes, a_scales, a_hp, M: int, w_codes, w_scales, w_hp, R, out=None, bias=None,
+                       gate=None, gate_rows: int | None = None, stream=None):
+    """R + gate * (the dual-branch product + bias) (osm_dual_gemm_residual). R: [M][N] BF16 or float32; out may be R."""
+    N = plan.N
+    dt = _stream_type(R, "R")
+    if out is None:
+        out = _new((M, N), R.dtype, R, stream)
+    g, rows, stride = _shared_rows(gate, "gate", M, N, gate_rows)
+    _check(lib().osm_dual_gemm_residual(plan.handle, *_packed_ptrs(plan, M, a_codes, a_scales, a_hp, "a"), M,
+                                        *_packed_ptrs(plan, N, w_codes, w_scales, w_hp, "w"),
+                                        _vector(bias, "bias", N), g, rows, stride, _operand(R, "R", None, (M, N)), dt,
+                                        _operand(out, "out", (R.dtype,), (M, N)), _stream(stream)))
+    return out
+
+
+def hp_plan(K: int, N: int) -> Plan:
+    """The plan of a layer kept in BF16: every channel on the outlier branch (k = K), no smoothing (s = 1)."""
+    return Plan(K, N, K, np.ones(K, np.float32), np.arange(K, dtype=np.int32))
+
+
+def linear_hp(plan: Plan, X, w_hp, bias=None, act: int = ACT_NONE, gate=None, gate_rows: int | None = None,
+              residual=None, out=None, dtype=None, stream=None):
+    """[residual +] [gate *] act(X W + bias) in BF16 (osm_linear_hp). plan: hp_plan(K, N); X: [M][K] BF16; w_hp: packed
+    by pack_weights; the output is BF16 or float32 (out's type, residual's, or dtype; BF16 by default). out may be
+    residual."""
+    import torch
+    M, N = X.shape[0], plan.N
+    if out is None:
+        out = _new((M, N), residual.dtype if residual is not None else dtype or torch.bfloat16, X, stream)
+    if dtype is not None and out.dtype != dtype:
+        raise ValueError(f"the output has dtype {out.dtype}, dtype says {dtype}")
+    if M < 1:
+        raise ValueError("X has no rows")
+    g, rows, stride = _shared_rows(gate, "gate", M, N, gate_rows)
+    _here(w_hp, "w_hp")
+    _check(lib().osm_linear_hp(plan.handle, _operand(X, "X", _bf16_types(), (M, plan.K)), M,
+                               _ptr(w_hp, "w_hp", _bf16_types(), plan.sizes(N)[2]), _vector(bias, "bias", N), int(act),
+                               g, rows, stride, _operand(residual, "residual", (out.dtype,), (M, N), allow_none=True),
+                               _operand(out, "out", None, (M, N)), _stream_type(out, "out"), _stream(stream)))
+    return out
+
+
+def ffn_sublayer(up: Plan, down: Plan, R, norm: Norm, wu, wd, workspace, out=None, bias_down=None, gate=None,
+                 gate_rows: int | None = None, stream=None):
+    """R + gate * (FFN(norm(R)) + bias_down) (osm_ffn_sublayer): the weights and the workspace of ffn_block. R: [M][D]
+    BF16 or float32; out may be R."""
+    M, D = R.shape
+    if D != up.K:
+        raise ValueError("R must have up.K columns")
+    if out is None:
+        out = _new((M, D), R.dtype, R, stream)
+    _here(workspace, "workspace")
+    g, rows, stride = _shared_rows(gate, "gate", M, D, gate_rows)
+    _check(lib().osm_ffn_sublayer(up.handle, down.handle, ctypes.byref(norm.spec(M, D)), _operand(R, "R", None, (M, D)),
+                                  _stream_type(R, "R"), M, *_packed_ptrs(up, up.N, *wu, "wu"),
+                                  *_packed_ptrs(down, down.N, *wd, "wd"), _vector(bias_down, "bias_down", down.N), g,
+                                  rows, stride, _operand(out, "out", (R.dtype,), (M, D)), _ptr(workspace, "workspace"),
+                                  workspace.numel() * workspace.element_size(), _stream(stream)))
+    return out
+
+
 # ----------------------------------------------------------------- composition
 
 def calibrate(X_batches, W, alpha: float, k: int, stream=None):
@@ -566,7 +781,9 @@ def calibrate(X_batches, W, alpha: float, k: int, stream=None):
 
 class QuantLinear:
     """A packed layer: plan + resident packed weights. `forward(X)` runs
-    quantize_act and dual_gemm on the current stream."""
+    quantize_act and dual_gemm on the current stream; with `norm` the rows
+    are normalised on the way (norm_quantize_act), with `residual` the
+    product is gated and added to it (dual_gemm_residual)."""
 
     def __init__(self, plan: Plan, W, bias=None, device="cuda"):
         self.plan = plan
@@ -574,14 +791,39 @@ class QuantLinear:
         pack_weights(plan, W, self.w_codes, self.w_scales, self.w_hp)
         self.bias = bias
 
-    def forward(self, X, epi: int = EPI_F32, out=None, act_buffers=None, stream=None):
+    def forward(self, X, epi: int = EPI_F32, out=None, act_buffers=None, stream=None, norm: Norm | None = None,
+                residual=None, gate=None, gate_rows: int | None = None):
         import torch
         M = X.shape[0]
+        if residual is None and gate is not None:
+            raise ValueError("gate goes with residual")
         a = act_buffers if act_buffers is not None else self.plan.alloc_packed(M, X.device)
-        quantize_act(self.plan, X, *a, stream=stream)
+        if norm is not None:
+            norm_quantize_act(self.plan, X, norm, *a, stream=stream)
+        else:
+            quantize_act(self.plan, X, *a, stream=stream)
+        if residual is not None:
+            return dual_gemm_residual(self.plan, *a, M, self.w_codes, self.w_scales, self.w_hp, residual, out=out,
+                                      bias=self.bias, gate=gate, gate_rows=gate_rows, stream=stream)
         if out is None:
             out = torch.empty((M, self.plan.N), dtype=torch.float32 if epi == EPI_F32 else torch.bfloat16,
                               device=X.device)
         dual_gemm(self.plan, *a, M, self.w_codes, self.w_scales, self.w_hp, out, bias=self.bias, epi=epi,
                   stream=stream)
         return out
+
+
+class HpLinear:
+    """A layer kept in BF16: plan + resident packed weights W [K][N]. `forward(X)` runs linear_hp on the current
+    stream."""
+
+    def __init__(self, W, bias=None):
+        K, N = W.shape
+        self.plan = hp_plan(K, N)
+        codes, scales, self.w_hp = self.plan.alloc_packed(N, W.device)
+        pack_weights(self.plan, W, codes, scales, self.w_hp)
+        self.bias = bias
+
+    def forward(self, X, act: int = ACT_NONE, gate=None, gate_rows=None, residual=None, out=None, dtype=None,
+                stream=None):
+        return linear_hp(self.plan, X, self.w_hp, self.bias, act, gate, gate_rows, residual, out, dtype, stream)

@@ -43,7 +43,7 @@ float pow2f(int g) { return std::ldexp(1.0f, g); }
 float nvfp4_k(int g) { return std::ldexp(1.0f / 6.0f, -g); }
 
 // The kernels are built for sm_100a only.
-static int check_device() {
+int check_device() {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return fail(OSM_ERR_CUDA, "no CUDA device");
     int major = 0, minor = 0;
@@ -55,24 +55,13 @@ static int check_device() {
     return OSM_OK;
 }
 
-static int check_plan(const osm_plan* p) {
+int check_plan(const osm_plan* p) {
     if (!p) return fail(OSM_ERR_INVALID_ARG, "plan is NULL");
     int dev = -1;
     cudaGetDevice(&dev);
     if (dev != p->device) return fail(OSM_ERR_INVALID_ARG, "plan belongs to device %d, current is %d", p->device, dev);
     return OSM_OK;
 }
-
-#define OSM_REQUIRE(cond, ...)                                        \
-    do {                                                              \
-        if (!(cond)) return fail(OSM_ERR_INVALID_ARG, __VA_ARGS__);   \
-    } while (0)
-
-#define OSM_TRY(expr)             \
-    do {                          \
-        int rc_ = (expr);         \
-        if (rc_) return rc_;      \
-    } while (0)
 
 }  // namespace osm
 
@@ -187,6 +176,7 @@ int osm_plan_create(int64_t K, int64_t N, int64_t k, const float* s_host, const 
     p->fmt = OSM_FMT_MXFP4;
     p->g_act = 0;
     p->g_w = 0;
+    p->unit_s = std::all_of(s_host, s_host + K, [](float v) { return v == 1.0f; });
     p->wait_limit_ns = 2000000000ull;
     p->debug_flags = 0;
 
@@ -427,6 +417,7 @@ int osm_plan_refresh_scored(osm_plan* p, const float* amax, const float* score, 
     auto ok = [](const float* x) { return x && (reinterpret_cast<uintptr_t>(x) & 3) == 0; };
     OSM_REQUIRE(ok(amax) && ok(score) && ok(wmax), "plan_refresh: amax / score / wmax null or misaligned");
     OSM_REQUIRE(alpha > 0.0f && alpha < 1.0f, "plan_refresh: alpha must lie in (0, 1)");
+    p->unit_s = 0;
     return launch_plan_refresh(p, amax, score, wmax, alpha, static_cast<cudaStream_t>(stream));
 }
 

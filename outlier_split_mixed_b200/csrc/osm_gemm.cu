@@ -46,6 +46,7 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 
 #include "osm_internal.h"
 #include "osm_mx.cuh"
@@ -168,6 +169,7 @@ struct GemmParams {
     int nKb, nKbp, nk, nkp;   // next's bulk / outlier widths
     int next_hp_fp16;         // next's outlier slots in binary16
     int64_t m_pad;            // M rounded up to 128 (rows of next_scales)
+    Onto onto;                // EPI_ONTO_*: the residual stream and its gate
 };
 
 __device__ __forceinline__ void tile_coords(int tile, int num_m, int num_n, int group_m, int& m_blk, int& n_blk) {
@@ -251,6 +253,83 @@ __device__ __forceinline__ void store_slab(const GemmParams& p, int64_t row0, in
             if (rb < p.M) *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.Y) + rb * p.N + col) = mx::bf16x2_bits(b.x, b.y);
         }
     }
+}
+// EPI_ONTO_*: Y = r + gate * (acc + bias) for one slab, laid out as in
+// store_slab. The residual words of B column blocks are loaded before the
+// first of them is used, so that their latencies overlap; a thread reads
+// each word of r before it writes the same word of Y, so Y may be r. The
+// product is gated and added in FP32 and rounded once, to the stream's type.
+template <int EPI, bool NV>
+__device__ __forceinline__ void onto_slab(const GemmParams& p, int64_t row0, int64_t col0, int lane, const uint32_t* r) {
+    constexpr bool F32 = EPI == EPI_ONTO_F32;
+    constexpr int B = F32 ? 4 : 8;
+    const int64_t ra = row0 + (lane >> 2), rb = ra + 8;
+    const int cq = 2 * (lane & 3);
+    const bool on_a = ra < p.M, on_b = rb < p.M;
+    const float *gate_a = nullptr, *gate_b = nullptr;
+    if (p.onto.gate) {  // rows past M read the last row's gate
+        const uint32_t last = static_cast<uint32_t>(p.M - 1), share = static_cast<uint32_t>(p.onto.gate_rows);
+        gate_a = p.onto.gate + (min(static_cast<uint32_t>(ra), last) / share) * p.onto.gate_stride;
+        gate_b = p.onto.gate + (min(static_cast<uint32_t>(rb), last) / share) * p.onto.gate_stride;
+    }
+    using Word = typename std::conditional<F32, float2, uint32_t>::type;
+    const Word* res = static_cast<const Word*>(p.onto.r);
+    Word* out = static_cast<Word*>(p.Y);
+    const int64_t ia = ra * (p.N >> 1), ib = rb * (p.N >> 1);
+#pragma unroll
+    for (int j0 = 0; j0 < 16; j0 += B) {
+        Word wa[B], wb[B];
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            const int64_t col = col0 + 8 * (j0 + i) + cq;
+            if (col < p.N) {
+                if (on_a) wa[i] = res[ia + (col >> 1)];
+                if (on_b) wb[i] = res[ib + (col >> 1)];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            const int j = j0 + i;
+            const int64_t col = col0 + 8 * j + cq;
+            if (col >= p.N) break;
+            float2 a = make_float2(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]));
+            float2 b = make_float2(__uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
+            if constexpr (NV) {
+                a = __fmul2_rn(a, make_float2(p.out_scale, p.out_scale));
+                b = __fmul2_rn(b, make_float2(p.out_scale, p.out_scale));
+            }
+            if (p.bias) {
+                const float2 bb = __ldg(reinterpret_cast<const float2*>(p.bias + col));
+                a = __fadd2_rn(a, bb);
+                b = __fadd2_rn(b, bb);
+            }
+            if (p.onto.gate) {
+                a = __fmul2_rn(a, __ldg(reinterpret_cast<const float2*>(gate_a + col)));
+                b = __fmul2_rn(b, __ldg(reinterpret_cast<const float2*>(gate_b + col)));
+            }
+            auto add = [](float2 v, Word w) {
+                if constexpr (F32) return __fadd2_rn(w, v);
+                else return __fadd2_rn(make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)), v);
+            };
+            auto put = [&](int64_t at, float2 v) {
+                if constexpr (F32) out[at + (col >> 1)] = v;
+                else out[at + (col >> 1)] = mx::bf16x2_bits(v.x, v.y);
+            };
+            if (on_a) put(ia, add(a, wa[i]));
+            if (on_b) put(ib, add(b, wb[i]));
+        }
+    }
+}
+// Bring a warp's part of the residual tile (32 rows x 128 columns) into L2
+// while its accumulator is still being computed.
+template <bool F32>
+__device__ __forceinline__ void prefetch_residual(const GemmParams& p, int64_t y0, int64_t x0, int lane) {
+    const int64_t row = y0 + lane;
+    if (row >= p.M || x0 >= p.N) return;
+    constexpr int W = F32 ? 4 : 2;
+    const char* at = static_cast<const char*>(p.onto.r) + (row * p.N + x0) * W;
+    const int bytes = static_cast<int>(min(static_cast<int64_t>(128), p.N - x0)) * W;
+    for (int o = 0; o < bytes; o += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + o));
 }
 // Wait for this warp's tensor-memory loads, then tell the leader CTA's
 // MMA warp that the accumulator may be overwritten (16 arrivals: 8 warps in
@@ -555,6 +634,9 @@ __device__ __forceinline__ void epilogue_role(const GemmParams& p, Smem<NV>& S, 
     for (int tile = pair; tile < tiles; tile += npairs) {
         int m_blk, n_blk;
         tile_coords(tile, p.num_m, p.num_n, p.group_m, m_blk, n_blk);
+        if constexpr (EPI == EPI_ONTO_BF16 || EPI == EPI_ONTO_F32)
+            prefetch_residual<EPI == EPI_ONTO_F32>(p, (int64_t)m_blk * 2 * BM + (int64_t)rank * BM + q * 32,
+                                                   (int64_t)n_blk * BN + half * 128, lane);
         int ok = 1;
         if (lane == 0)
             // the accumulator completes once per tile (about 10 us of MMAs):
@@ -595,7 +677,10 @@ __device__ __forceinline__ void epilogue_role(const GemmParams& p, Smem<NV>& S, 
             if (x0 < p.N) {
 #pragma unroll 1
                 for (int sl = 0; sl < 2; ++sl) {
-                    store_slab<EPI, NV>(p, y0 + 16 * sl, x0, lane, r);
+                    if constexpr (EPI == EPI_ONTO_BF16 || EPI == EPI_ONTO_F32)
+                        onto_slab<EPI, NV>(p, y0 + 16 * sl, x0, lane, r);
+                    else
+                        store_slab<EPI, NV>(p, y0 + 16 * sl, x0, lane, r);
                     shift_down<64>(r);
                 }
             }
@@ -701,21 +786,6 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn() {
     return fn;
 }
 
-int make_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t rows,
-             uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swz,
-             const char* what) {
-    auto enc = get_encode_fn();
-    if (!enc) return fail(OSM_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
-    cuuint64_t dims[2] = {inner, rows};
-    cuuint64_t strides[1] = {row_stride_bytes};
-    cuuint32_t box[2] = {box_inner, box_rows};
-    cuuint32_t estr[2] = {1, 1};
-    CUresult r = enc(m, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
-                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return fail(OSM_ERR_CUDA, "tensor map for %s: CUresult %d", what, (int)r);
-    return OSM_OK;
-}
-
 struct LaunchInfo {
     int max_pairs = 0;
     bool ready = false;
@@ -734,6 +804,20 @@ __global__ void gelu_f32_kernel(const float* __restrict__ x, float* __restrict__
 
 }  // namespace
 
+int make_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t rows,
+             uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swz,
+             const char* what) {
+    auto enc = get_encode_fn();
+    if (!enc) return fail(OSM_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+    cuuint64_t dims[2] = {inner, rows};
+    cuuint64_t strides[1] = {row_stride_bytes};
+    cuuint32_t box[2] = {box_inner, box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = enc(m, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(OSM_ERR_CUDA, "tensor map for %s: CUresult %d", what, (int)r);
+    return OSM_OK;
+}
 
 int launch_gelu_f32(const float* x, float* y, int64_t n, cudaStream_t st) {
     const int64_t blocks = std::min<int64_t>((n + 511) / 512, 148 * 8);
@@ -744,7 +828,7 @@ int launch_gelu_f32(const float* x, float* y, int64_t n, cudaStream_t st) {
 int launch_dual_gemm(const osm_plan* pl, const uint8_t* a_codes, const uint8_t* a_scales, const uint16_t* a_hp,
                      int64_t M, const uint8_t* w_codes, const uint8_t* w_scales, const uint16_t* w_hp,
                      const float* bias, int epi, void* Y, const osm_plan* next, uint8_t* next_codes,
-                     uint8_t* next_scales, uint16_t* next_hp, cudaStream_t st) {
+                     uint8_t* next_scales, uint16_t* next_hp, cudaStream_t st, const Onto* onto) {
     static_assert(sizeof(Smem<false>) + 1024 <= 232448 && sizeof(Smem<true>) + 1024 <= 232448,
                   "shared memory budget");
     const bool nv = pl->fmt == OSM_FMT_NVFP4;
@@ -797,6 +881,7 @@ int launch_dual_gemm(const osm_plan* pl, const uint8_t* a_codes, const uint8_t* 
     }
     p.n_row_tiles = static_cast<int>(ceil_div(pl->N, 128));
     p.epi = epi;
+    if (onto) p.onto = *onto;
     p.idesc_hp = pl->hp_fp16 ? IDESC_F16 : IDESC_BF16;
     p.out_scale = nv ? pow2f(pl->g_act + pl->g_w) : 1.0f;
     if (epi == OSM_EPI_GELU_REQUANT) {
@@ -827,11 +912,17 @@ int launch_dual_gemm(const osm_plan* pl, const uint8_t* a_codes, const uint8_t* 
         case OSM_EPI_GELU_BF16:
             kernel = nv ? dual_gemm_kernel<OSM_EPI_GELU_BF16, true> : dual_gemm_kernel<OSM_EPI_GELU_BF16, false>;
             break;
+        case EPI_ONTO_BF16:
+            kernel = nv ? dual_gemm_kernel<EPI_ONTO_BF16, true> : dual_gemm_kernel<EPI_ONTO_BF16, false>;
+            break;
+        case EPI_ONTO_F32:
+            kernel = nv ? dual_gemm_kernel<EPI_ONTO_F32, true> : dual_gemm_kernel<EPI_ONTO_F32, false>;
+            break;
         default: return fail(OSM_ERR_INVALID_ARG, "dual_gemm: epilogue %d", epi);
     }
 
     // co-resident clusters of two CTAs, queried once per device and epilogue
-    static LaunchInfo info[64][8];
+    static LaunchInfo info[64][12];
     static std::mutex mu;
     int dev = 0;
     if ((rc = check_cuda(cudaGetDevice(&dev), "cudaGetDevice"))) return rc;

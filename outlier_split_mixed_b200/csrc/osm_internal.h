@@ -3,6 +3,7 @@
 
 #include <cstdint>
 #include <cstddef>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "osm.h"
@@ -27,6 +28,7 @@ struct osm_plan {
     uint32_t* d_status;  // OSM_STATUS_* bits written by kernels
     float* d_s_new;      // [3K] scratch of osm_plan_refresh: s, inv_s, then the channels' ranks (int32)
     uint32_t* d_bad;     // scratch of osm_plan_refresh: a statistic was not finite
+    int unit_s;          // s == 1 for every channel: x' = x (osm_linear_hp reads X itself)
     uint64_t wait_limit_ns;
     uint32_t debug_flags;  // OSM_DEBUG_* (failure-detection tests)
 };
@@ -41,6 +43,21 @@ constexpr int QA_BLOCK_BYTES = 80;
 void set_error(const char* fmt, ...);
 int fail(int code, const char* fmt, ...);
 int check_cuda(cudaError_t e, const char* what);
+
+// The kernels run on sm_100 only; a plan on the device it was made on.
+int check_device();
+int check_plan(const osm_plan* p);
+
+#define OSM_REQUIRE(cond, ...)                                        \
+    do {                                                              \
+        if (!(cond)) return fail(OSM_ERR_INVALID_ARG, __VA_ARGS__);   \
+    } while (0)
+
+#define OSM_TRY(expr)             \
+    do {                          \
+        int rc_ = (expr);         \
+        if (rc_) return rc_;      \
+    } while (0)
 
 inline int64_t round_up(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -59,6 +76,21 @@ inline int64_t scales_bytes(int64_t rows, int64_t Kbp, int fmt) {
 float nvfp4_k(int g);
 float pow2f(int g);
 
+// What an epilogue adds its product to: out = r + gate * y (either part may
+// be missing), row t taking gate row t / gate_rows.
+struct Onto {
+    const void* r;           // [M][N] in the output's type, or NULL
+    const float* gate;       // [rows / gate_rows][gate_stride], or NULL
+    int64_t gate_rows, gate_stride;
+};
+// Epilogues of the dual GEMM beyond osm_epi: onto a residual stream.
+constexpr int EPI_ONTO_BF16 = 4, EPI_ONTO_F32 = 5;
+
+// A two-dimensional tensor map (rows of `inner` elements) for tiled TMA copies.
+int make_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t rows,
+             uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swz,
+             const char* what);
+
 // launchers (return OSM_OK or an error code; arguments already validated)
 int launch_act_amax(const uint16_t* X, int64_t T, int64_t K, float* amax, cudaStream_t st);
 int launch_act_percentile(const uint16_t* X, int64_t T, int64_t K, int64_t rank, float* score, cudaStream_t st);
@@ -75,6 +107,13 @@ int launch_dual_gemm(const osm_plan* p, const uint8_t* a_codes, const uint8_t* a
                      const uint16_t* a_hp, int64_t M, const uint8_t* w_codes,
                      const uint8_t* w_scales, const uint16_t* w_hp, const float* bias, int epi,
                      void* Y, const osm_plan* next, uint8_t* next_codes, uint8_t* next_scales,
-                     uint16_t* next_hp, cudaStream_t st);
+                     uint16_t* next_hp, cudaStream_t st, const Onto* onto = nullptr);
+int launch_linear_hp(const osm_plan* p, const uint16_t* X, int64_t M, const uint16_t* w_hp, const float* bias, int act,
+                     const Onto& onto, void* Y, int y_dtype, cudaStream_t st);
+int launch_norm_quantize(const osm_plan* p, const void* X, int x_dtype, int64_t M, const osm_norm_spec* spec,
+                         uint8_t* codes, uint8_t* scales, uint16_t* hp, cudaStream_t st);
+int launch_norm_rows(const void* X, int x_dtype, int64_t M, int64_t D, const uint16_t* Y, const osm_norm_spec* post,
+                     const float* gate, int64_t gate_rows, int64_t gate_stride, float alpha,
+                     const osm_norm_spec* pre, void* R_out, uint16_t* H, cudaStream_t st);
 
 }  // namespace osm

@@ -1,0 +1,709 @@
+// The BF16 layers of a deployment (osm_linear_hp): Y = [R +] [gate] act(X W +
+// bias) on the tensor cores, W packed transposed [N][kp] by a k = K plan.
+//
+// Two kernels, by the number of tokens:
+//   pair_kernel   CTA pairs on 256 x 256 output tiles (tcgen05 cta_group::2),
+//                 persistent, two accumulators in tensor memory: the epilogue
+//                 of a tile runs under the MMAs of the next.
+//   skinny_kernel few tokens: the weights are what has to be read. The
+//                 operands change places -- 128 output channels are the rows
+//                 of the MMA, NT tokens its columns -- and the CTAs of a
+//                 cluster split K, so that every SM streams weights; the
+//                 partial sums are joined through distributed shared memory
+//                 in the order of the ranks.
+// Every wait is bounded by %globaltimer; one that runs out sets the plan's
+// status word and the CTA returns after its copies and MMAs have finished.
+// No TMA multicast is used.
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <cstring>
+#include <mutex>
+#include <type_traits>
+
+#include "osm_internal.h"
+#include "osm_mx.cuh"
+#include "osm_ptx.cuh"
+
+namespace osm {
+namespace {
+
+constexpr int KSTEP = 64;               // BF16 values of one 128-byte swizzled row
+constexpr int ROWS = 128;               // MMA rows per CTA (tensor-memory lanes)
+constexpr int TILE = ROWS * 128;        // bytes of one 128-row operand tile of a K-step
+constexpr uint16_t PAIR_MASK = 0x3;
+
+struct LinearParams {
+    CUtensorMap tm_x;    // X    [M][K] bf16
+    CUtensorMap tm_w;    // w_hp [N][kp] bf16, box 64 x 128
+    const float* bias;
+    void* Y;
+    Onto onto;
+    uint32_t* status;
+    uint64_t wait_limit_ns;
+    int64_t M, N;
+    int ksteps;
+    int act;
+    int num_m, num_n, group_m;  // pair_kernel: tiles and raster
+};
+
+__host__ __device__ constexpr uint32_t idesc_bf16(int m, int n) {
+    // kind::f16: FP32 accumulator, A and B BF16, both K-major
+    return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
+           (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
+    return ptx::smem_desc(saddr, 16, 1024, ptx::LAYOUT_SW128);
+}
+
+// x / (1 + 2^z) with z = -x log2(e); z is capped so that 1 + 2^z stays finite.
+__device__ __forceinline__ float2 silu2(float2 x) {
+    const float2 z = __fmul2_rn(x, make_float2(-1.44269504f, -1.44269504f));
+    const float2 d = __fadd2_rn(make_float2(mx::ex2_approx(fminf(z.x, 126.0f)), mx::ex2_approx(fminf(z.y, 126.0f))),
+                                make_float2(1.0f, 1.0f));
+    return __fmul2_rn(x, make_float2(mx::rcp_approx(d.x), mx::rcp_approx(d.y)));
+}
+__device__ __forceinline__ float2 activate2(float2 v, int act) {
+    if (act == OSM_ACT_GELU) return mx::gelu2(v);
+    if (act == OSM_ACT_SILU) return silu2(v);
+    return v;
+}
+
+// ------------------------------------------------------------ pair_kernel
+
+constexpr int PK_STAGES = 6;
+constexpr int PK_EPI_WARPS = 8;
+constexpr int PK_THREADS = 32 * PK_EPI_WARPS + 64;
+constexpr int PK_PRODUCER = PK_EPI_WARPS, PK_MMA = PK_EPI_WARPS + 1;
+constexpr int PK_N = 256;
+constexpr uint32_t PK_IDESC = idesc_bf16(256, PK_N);
+
+struct __align__(1024) PairSmem {
+    uint8_t a[PK_STAGES][TILE];
+    uint8_t b[PK_STAGES][TILE];  // this CTA's half of the 256 output channels
+    uint64_t full[PK_STAGES];    // leader: all copies of both CTAs for the slot have landed
+    uint64_t empty[PK_STAGES];   // both: the MMAs reading the slot have completed
+    uint64_t acc_full[2];        // both: an accumulator is complete
+    uint64_t acc_empty[2];       // leader: both CTAs have drained it
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+template <class SM>
+__device__ __forceinline__ void raise_abort(SM& S, uint32_t* status) {
+    S.abort_flag = 1;
+    atomicOr(status, OSM_STATUS_TIMEOUT);
+}
+
+__device__ __forceinline__ void pair_coords(const LinearParams& p, int tile, int& m, int& n) {
+    const int group = p.group_m * p.num_n, g = tile / group, first = g * p.group_m;
+    const int gm = min(p.num_m - first, p.group_m), local = tile % group;
+    m = first + local % gm;
+    n = local / gm;
+}
+
+// Sixteen tensor-memory lanes x 128 columns: thread t holds rows t / 4 and
+// t / 4 + 8 and, of each 8-column block j, columns 2 (t % 4) and the next
+// (registers 4j .. 4j + 3).
+__device__ __forceinline__ void tmem_ld_16x256b_x16(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+        "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+        "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+          "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+          "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+          "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(taddr));
+}
+
+// Epilogue of one 16-row x 128-column slab. The residual words of B column
+// blocks are loaded before the first is used; a thread reads each word of R
+// before it writes the same word of Y, so Y may be R. FP32 until the one
+// rounding to Y's type.
+template <bool F32>
+__device__ __forceinline__ void pair_slab(const LinearParams& p, int64_t row0, int64_t col0, int lane, const uint32_t* r) {
+    constexpr int B = F32 ? 4 : 8;
+    const int64_t ra = row0 + (lane >> 2), rb = ra + 8;
+    const int cq = 2 * (lane & 3);
+    const bool on_a = ra < p.M, on_b = rb < p.M;
+    const float *gate_a = nullptr, *gate_b = nullptr;
+    if (p.onto.gate) {  // rows past M read the last row's gate
+        const uint32_t last = static_cast<uint32_t>(p.M - 1), share = static_cast<uint32_t>(p.onto.gate_rows);
+        gate_a = p.onto.gate + (min(static_cast<uint32_t>(ra), last) / share) * p.onto.gate_stride;
+        gate_b = p.onto.gate + (min(static_cast<uint32_t>(rb), last) / share) * p.onto.gate_stride;
+    }
+    using Word = typename std::conditional<F32, float2, uint32_t>::type;
+    const Word* res = static_cast<const Word*>(p.onto.r);
+    Word* out = static_cast<Word*>(p.Y);
+    const int64_t ia = ra * (p.N >> 1), ib = rb * (p.N >> 1);
+#pragma unroll
+    for (int j0 = 0; j0 < 16; j0 += B) {
+        Word wa[B], wb[B];
+        if (res) {
+#pragma unroll
+            for (int i = 0; i < B; ++i) {
+                const int64_t col = col0 + 8 * (j0 + i) + cq;
+                if (col < p.N) {
+                    if (on_a) wa[i] = res[ia + (col >> 1)];
+                    if (on_b) wb[i] = res[ib + (col >> 1)];
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            const int j = j0 + i;
+            const int64_t col = col0 + 8 * j + cq;
+            if (col >= p.N) break;
+            float2 a = make_float2(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]));
+            float2 b = make_float2(__uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
+            if (p.bias) {
+                const float2 bb = __ldg(reinterpret_cast<const float2*>(p.bias + col));
+                a = __fadd2_rn(a, bb);
+                b = __fadd2_rn(b, bb);
+            }
+            a = activate2(a, p.act);
+            b = activate2(b, p.act);
+            if (p.onto.gate) {
+                a = __fmul2_rn(a, __ldg(reinterpret_cast<const float2*>(gate_a + col)));
+                b = __fmul2_rn(b, __ldg(reinterpret_cast<const float2*>(gate_b + col)));
+            }
+            auto add = [](float2 v, Word w) {
+                if constexpr (F32) return __fadd2_rn(w, v);
+                else return __fadd2_rn(make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)), v);
+            };
+            auto put = [&](int64_t at, float2 v) {
+                if constexpr (F32) out[at + (col >> 1)] = v;
+                else out[at + (col >> 1)] = mx::bf16x2_bits(v.x, v.y);
+            };
+            if (on_a) put(ia, res ? add(a, wa[i]) : a);
+            if (on_b) put(ib, res ? add(b, wb[i]) : b);
+        }
+    }
+}
+
+// Bring a warp's part of the residual tile (32 rows x 128 columns) into L2
+// while its accumulator is still being computed.
+template <bool F32>
+__device__ __forceinline__ void prefetch_residual(const LinearParams& p, int64_t y0, int64_t x0, int lane) {
+    const int64_t row = y0 + lane;
+    if (!p.onto.r || row >= p.M || x0 >= p.N) return;
+    constexpr int W = F32 ? 4 : 2;
+    const char* at = static_cast<const char*>(p.onto.r) + (row * p.N + x0) * W;
+    const int bytes = static_cast<int>(min(static_cast<int64_t>(128), p.N - x0)) * W;
+    for (int o = 0; o < bytes; o += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + o));
+}
+
+template <bool F32>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PK_THREADS, 1)
+    pair_kernel(const __grid_constant__ LinearParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    PairSmem& S = *reinterpret_cast<PairSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = ptx::cluster_ctarank();
+    const bool leader = rank == 0;
+    const int pair = static_cast<int>(ptx::cluster_id_x()), npairs = static_cast<int>(ptx::num_clusters_x());
+    const int tiles = p.num_m * p.num_n;
+    const volatile int* abort = &S.abort_flag;
+    __shared__ int never;
+    const uint64_t drain_ns = p.wait_limit_ns > 200000000ull ? p.wait_limit_ns : 200000000ull;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < PK_STAGES; ++s) {
+            ptx::mbar_init(ptx::smem_u32(&S.full[s]), 1);
+            ptx::mbar_init(ptx::smem_u32(&S.empty[s]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(ptx::smem_u32(&S.acc_full[i]), 1);
+            ptx::mbar_init(ptx::smem_u32(&S.acc_empty[i]), 2 * PK_EPI_WARPS);
+        }
+        ptx::mbar_init(ptx::smem_u32(&S.drain), 1);
+        S.abort_flag = 0;
+        never = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == PK_PRODUCER && lane == 0) {
+        ptx::prefetch_tmap(&p.tm_x);
+        ptx::prefetch_tmap(&p.tm_w);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc_pair(ptx::smem_u32(&S.tmem_base), 512);
+        ptx::tmem_relinquish_pair();
+    }
+    __syncwarp();
+    ptx::tc_fence_before();
+    ptx::cluster_sync();
+    ptx::tc_fence_after();
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    const uint32_t tmem = S.tmem_base;
+
+    if (warp == PK_PRODUCER) {
+        if (ptx::elect_one()) {
+            int stage = 0, last_stage = -1;
+            uint32_t phase = 0, last_phase = 0;
+            bool ok = true;
+            for (int tile = pair; tile < tiles && ok; tile += npairs) {
+                int m, n;
+                pair_coords(p, tile, m, n);
+                const int arow = m * 256 + static_cast<int>(rank) * ROWS;
+                const int brow = n * PK_N + static_cast<int>(rank) * ROWS;
+                for (int ks = 0; ks < p.ksteps; ++ks) {
+                    if (!ptx::mbar_wait_bounded(ptx::smem_u32(&S.empty[stage]), phase ^ 1u, p.wait_limit_ns, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t fb = ptx::mapa(ptx::smem_u32(&S.full[stage]), 0);
+                    if (leader) ptx::mbar_arrive_expect_tx(ptx::smem_u32(&S.full[stage]), 4u * TILE);
+                    ptx::tma_load_2d_pair(ptx::smem_u32(S.a[stage]), &p.tm_x, ks * KSTEP, arow, fb);
+                    ptx::tma_load_2d_pair(ptx::smem_u32(S.b[stage]), &p.tm_w, ks * KSTEP, brow, fb);
+                    last_stage = stage;
+                    last_phase = phase;
+                    if (++stage == PK_STAGES) { stage = 0; phase ^= 1u; }
+                }
+            }
+            if (!ok) raise_abort(S, p.status);
+            // the slot filled last is released after the MMAs that read it: by then every copy has landed
+            if (last_stage >= 0 &&
+                !ptx::mbar_wait_bounded_cluster(ptx::smem_u32(&S.empty[last_stage]), last_phase, drain_ns, &never))
+                ptx::spin_ns(1000000);
+        }
+    } else if (warp == PK_MMA) {
+        if (leader && ptx::elect_one()) {
+            int stage = 0, it = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int tile = pair; tile < tiles && ok; tile += npairs, ++it) {
+                const int buf = it & 1;
+                if (!ptx::mbar_wait_bounded_cluster(ptx::smem_u32(&S.acc_empty[buf]), ((it >> 1) & 1) ^ 1u,
+                                                    p.wait_limit_ns, abort)) {
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+                const uint32_t acc = tmem + buf * PK_N;
+                for (int ks = 0; ks < p.ksteps; ++ks) {
+                    if (!ptx::mbar_wait_bounded(ptx::smem_u32(&S.full[stage]), phase, p.wait_limit_ns, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after();
+                    const uint32_t a = ptx::smem_u32(S.a[stage]), b = ptx::smem_u32(S.b[stage]);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        ptx::mma_bf16_pair(acc, desc_sw128(a + kk * 32), desc_sw128(b + kk * 32), PK_IDESC,
+                                           (ks | kk) != 0);
+                    ptx::tc_commit_pair_mc(ptx::smem_u32(&S.empty[stage]), PAIR_MASK);
+                    if (++stage == PK_STAGES) { stage = 0; phase ^= 1u; }
+                }
+                if (!ok) break;
+                ptx::tc_commit_pair_mc(ptx::smem_u32(&S.acc_full[buf]), PAIR_MASK);
+            }
+            if (!ok) raise_abort(S, p.status);
+            ptx::tc_commit_pair_mc(ptx::smem_u32(&S.drain), 0x1);
+            ptx::mbar_wait_bounded(ptx::smem_u32(&S.drain), 0, drain_ns, &never);
+        }
+    } else {
+        const int q = warp & 3, half = warp >> 2;
+        const uint32_t empty_leader[2] = {ptx::mapa(ptx::smem_u32(&S.acc_empty[0]), 0),
+                                          ptx::mapa(ptx::smem_u32(&S.acc_empty[1]), 0)};
+        int it = 0;
+        for (int tile = pair; tile < tiles; tile += npairs, ++it) {
+            int m, n;
+            pair_coords(p, tile, m, n);
+            const int buf = it & 1;
+            const int64_t y0 = (int64_t)m * 256 + (int64_t)rank * ROWS + q * 32;
+            const int64_t x0 = (int64_t)n * PK_N + half * 128;
+            prefetch_residual<F32>(p, y0, x0, lane);
+            int ok = 1;
+            if (lane == 0)
+                ok = ptx::mbar_wait_bounded_long(ptx::smem_u32(&S.acc_full[buf]), (it >> 1) & 1, p.wait_limit_ns, abort,
+                                                 20000u);
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) {
+                if (lane == 0) raise_abort(S, p.status);
+                break;
+            }
+            ptx::tc_fence_after();
+            const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * PK_N + half * 128;
+#pragma unroll 1
+            for (int sl = 0; sl < 2; ++sl) {
+                uint32_t r[64];
+                tmem_ld_16x256b_x16(taddr + (static_cast<uint32_t>(16 * sl) << 16), r);
+                ptx::tmem_ld_wait();
+                if (sl == 1) {  // drained: the MMAs of the tile after next may overwrite it
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive_remote_relaxed(empty_leader[buf]);
+                }
+                if (x0 < p.N) pair_slab<F32>(p, y0 + 16 * sl, x0, lane, r);
+            }
+        }
+    }
+    __syncwarp();
+    ptx::tc_fence_before();
+    ptx::cluster_sync();
+    if (warp == 1) {
+        __syncwarp();
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+// ------------------------------------------------------------ skinny_kernel
+
+constexpr int SK_THREADS = 192;  // warps 0-3 drain tensor memory, 4 issues the copies, 5 the MMAs
+
+// Ring slots: as many as leave room for two CTAs per SM (one for 256 tokens).
+__host__ __device__ constexpr int sk_stages(int nt) { return nt <= 32 ? 5 : (nt <= 64 ? 4 : (nt == 128 ? 3 : 4)); }
+
+template <int NT>
+struct __align__(1024) SkinnySmem {
+    static constexpr int STAGES = sk_stages(NT);
+    union {
+        struct {
+            uint8_t w[STAGES][TILE];
+            uint8_t x[STAGES][NT * 128];
+        } ring;
+        float part[NT][ROWS];  // the CTA's partial sums, token-major, once the ring is idle
+    };
+    uint64_t full[STAGES];
+    uint64_t empty[STAGES];
+    uint64_t done;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+// Grid: x = clusters of S CTAs over the 128-channel tiles, y = token tiles.
+// Rank s of a cluster takes the K-steps [s ks / S, (s + 1) ks / S).
+template <int NT, bool F32>
+__global__ void __launch_bounds__(SK_THREADS) skinny_kernel(const __grid_constant__ LinearParams p, int splits) {
+    using SM = SkinnySmem<NT>;
+    constexpr int STAGES = SM::STAGES;
+    constexpr uint32_t COLS = NT < 32 ? 32 : NT;
+    extern __shared__ uint8_t smem_raw[];
+    SM& S = *reinterpret_cast<SM*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = splits > 1 ? static_cast<int>(ptx::cluster_ctarank()) : 0;
+    const int n0 = (static_cast<int>(blockIdx.x) / splits) * ROWS;
+    const int m0 = static_cast<int>(blockIdx.y) * NT;
+    const int k0 = static_cast<int>(static_cast<int64_t>(p.ksteps) * rank / splits);
+    const int k1 = static_cast<int>(static_cast<int64_t>(p.ksteps) * (rank + 1) / splits);
+    const volatile int* abort = &S.abort_flag;
+    __shared__ int never;
+    const uint64_t drain_ns = p.wait_limit_ns > 200000000ull ? p.wait_limit_ns : 200000000ull;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            ptx::mbar_init(ptx::smem_u32(&S.full[s]), 1);
+            ptx::mbar_init(ptx::smem_u32(&S.empty[s]), 1);
+        }
+        ptx::mbar_init(ptx::smem_u32(&S.done), 1);
+        S.abort_flag = 0;
+        never = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 4 && lane == 0) {
+        ptx::prefetch_tmap(&p.tm_x);
+        ptx::prefetch_tmap(&p.tm_w);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(ptx::smem_u32(&S.tmem_base), COLS);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    const uint32_t tmem = S.tmem_base;
+
+    if (warp == 4) {
+        if (ptx::elect_one()) {
+            int stage = 0, issued = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int ks = k0; ks < k1; ++ks, ++issued) {
+                if (!ptx::mbar_wait_bounded(ptx::smem_u32(&S.empty[stage]), phase ^ 1u, p.wait_limit_ns, abort)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t fb = ptx::smem_u32(&S.full[stage]);
+                ptx::mbar_arrive_expect_tx(fb, TILE + NT * 128);
+                ptx::tma_load_2d(ptx::smem_u32(S.ring.w[stage]), &p.tm_w, ks * KSTEP, n0, fb);
+                ptx::tma_load_2d(ptx::smem_u32(S.ring.x[stage]), &p.tm_x, ks * KSTEP, m0, fb);
+                if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+            }
+            if (!ok) raise_abort(S, p.status);
+            // every copy has landed before the ring is used again (the MMAs wait for each of them;
+            // an aborted pipeline may not have)
+            for (int i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
+                if (!ptx::mbar_wait_bounded(ptx::smem_u32(&S.full[i % STAGES]), (i / STAGES) & 1, drain_ns, &never))
+                    ptx::spin_ns(1000000);
+        }
+    } else if (warp == 5) {
+        if (ptx::elect_one()) {
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int ks = k0; ks < k1; ++ks) {
+                if (!ptx::mbar_wait_bounded(ptx::smem_u32(&S.full[stage]), phase, p.wait_limit_ns, abort)) {
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+                const uint32_t a = ptx::smem_u32(S.ring.w[stage]), b = ptx::smem_u32(S.ring.x[stage]);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    ptx::mma_bf16(tmem, desc_sw128(a + kk * 32), desc_sw128(b + kk * 32), idesc_bf16(ROWS, NT),
+                                  (ks != k0 || kk != 0) ? 1u : 0u);
+                ptx::tc_commit(ptx::smem_u32(&S.empty[stage]));
+                if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+            }
+            if (!ok) raise_abort(S, p.status);
+            ptx::tc_commit(ptx::smem_u32(&S.done));
+            if (!ptx::mbar_wait_bounded(ptx::smem_u32(&S.done), 0, drain_ns, &never)) raise_abort(S, p.status);
+        }
+    }
+    // All copies have landed and all MMAs completed: the ring becomes the
+    // partial sums' buffer.
+    __syncwarp();
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    if (warp < 4) {
+        const uint32_t taddr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+#pragma unroll 1
+        for (int c = 0; c < NT; c += 32) {
+            uint32_t r[32];
+            ptx::tmem_ld_32x32b_x32(taddr + c, r);
+            ptx::tmem_ld_wait();
+            const bool some = k1 > k0;  // a rank without K-steps adds zeros
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (c + i < NT && m0 + c + i < p.M) S.part[c + i][warp * 32 + lane] = some ? __uint_as_float(r[i]) : 0.0f;
+        }
+        ptx::tc_fence_before();
+    }
+    if (splits > 1) ptx::cluster_sync();
+    else __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, COLS);
+    }
+    // Each rank finishes its share of the tile: four channels of one token at a time.
+    const int mt = static_cast<int>(min(static_cast<int64_t>(NT), p.M - m0));
+    const int total = mt * (ROWS / 4), chunk = (total + splits - 1) / splits;
+    const int end = min(total, (rank + 1) * chunk);
+    const uint32_t part0 = ptx::smem_u32(&S.part[0][0]);
+    for (int e = rank * chunk + static_cast<int>(threadIdx.x); e < end; e += SK_THREADS) {
+        const int t = e / (ROWS / 4), c = (e % (ROWS / 4)) * 4;
+        const int64_t n = n0 + c, m = m0 + t;
+        if (n >= p.N) continue;
+        const uint32_t off = part0 + (t * ROWS + c) * 4;
+        float4 v;
+        if (splits == 1) {
+            v = *reinterpret_cast<const float4*>(&S.part[t][c]);
+        } else {
+            v = ld_cluster_f4(ptx::mapa(off, 0));
+            for (int s = 1; s < splits; ++s) {
+                const float4 o = ld_cluster_f4(ptx::mapa(off, s));
+                v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+            }
+        }
+        float2 a = make_float2(v.x, v.y), b = make_float2(v.z, v.w);
+        if (p.bias) {
+            const float4 bb = __ldg(reinterpret_cast<const float4*>(p.bias + n));
+            a = __fadd2_rn(a, make_float2(bb.x, bb.y));
+            b = __fadd2_rn(b, make_float2(bb.z, bb.w));
+        }
+        a = activate2(a, p.act);
+        b = activate2(b, p.act);
+        if (p.onto.gate) {
+            const float4 g = __ldg(reinterpret_cast<const float4*>(
+                p.onto.gate + (static_cast<uint32_t>(m) / static_cast<uint32_t>(p.onto.gate_rows)) * p.onto.gate_stride + n));
+            a = __fmul2_rn(a, make_float2(g.x, g.y));
+            b = __fmul2_rn(b, make_float2(g.z, g.w));
+        }
+        const int64_t at = m * p.N + n;
+        if constexpr (F32) {
+            if (p.onto.r) {
+                const float4 w = *reinterpret_cast<const float4*>(static_cast<const float*>(p.onto.r) + at);
+                a = __fadd2_rn(make_float2(w.x, w.y), a);
+                b = __fadd2_rn(make_float2(w.z, w.w), b);
+            }
+            *reinterpret_cast<float4*>(static_cast<float*>(p.Y) + at) = make_float4(a.x, a.y, b.x, b.y);
+        } else {
+            if (p.onto.r) {
+                const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.onto.r) + at);
+                a = __fadd2_rn(make_float2(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u)), a);
+                b = __fadd2_rn(make_float2(__uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u)), b);
+            }
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.Y) + at) =
+                make_uint2(mx::bf16x2_bits(a.x, a.y), mx::bf16x2_bits(b.x, b.y));
+        }
+    }
+    // a CTA's partial sums stay until every rank has read them
+    if (splits > 1) ptx::cluster_sync();
+}
+
+// ------------------------------------------------------------ host
+
+struct KernelInfo {
+    int clusters = 0;  // co-resident CTA pairs (pair_kernel); 1 once prepared (skinny_kernel)
+    bool ready = false;
+};
+
+int current_device(int* dev) {
+    OSM_TRY(check_cuda(cudaGetDevice(dev), "cudaGetDevice"));
+    if (*dev < 0 || *dev >= 64) return fail(OSM_ERR_UNSUPPORTED, "device index %d", *dev);
+    return OSM_OK;
+}
+
+// Larger weights than this are swept by groups of M-tiles (see osm_gemm.cu).
+constexpr int64_t W_RESIDENT_BYTES = 48ll << 20;
+
+int launch_pair(LinearParams& p, bool f32, int64_t w_bytes, cudaStream_t st) {
+    void (*kern)(LinearParams) = f32 ? pair_kernel<true> : pair_kernel<false>;
+    constexpr size_t smem = sizeof(PairSmem) + 1024;
+    static_assert(smem <= 232448, "shared memory budget");
+    static KernelInfo info[64][2];
+    static std::mutex mu;
+    int dev = 0;
+    OSM_TRY(current_device(&dev));
+    KernelInfo& ki = info[dev][f32 ? 1 : 0];
+    {
+        std::lock_guard<std::mutex> lk(mu);
+        if (!ki.ready) {
+            OSM_TRY(check_cuda(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                    static_cast<int>(smem)), "linear_hp smem attribute"));
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(2, 1, 1);
+            cfg.blockDim = dim3(PK_THREADS, 1, 1);
+            cfg.dynamicSmemBytes = smem;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = 2;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            OSM_TRY(check_cuda(cudaOccupancyMaxActiveClusters(&ki.clusters, kern, &cfg), "linear_hp cluster occupancy"));
+            if (ki.clusters < 1) return fail(OSM_ERR_UNSUPPORTED, "linear_hp: no CTA pair fits on this device");
+            ki.ready = true;
+        }
+    }
+    p.num_m = static_cast<int>(ceil_div(p.M, 256));
+    p.num_n = static_cast<int>(ceil_div(p.N, PK_N));
+    p.group_m = w_bytes <= W_RESIDENT_BYTES ? 1 : 8;
+    const int64_t tiles = static_cast<int64_t>(p.num_m) * p.num_n;
+    if (tiles > 0x7FFFFFFF) return fail(OSM_ERR_UNSUPPORTED, "linear_hp: too many tiles");
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min<int64_t>(tiles, ki.clusters)), 1, 1);
+    cfg.blockDim = dim3(PK_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return check_cuda(cudaLaunchKernelEx(&cfg, kern, p), "linear_hp launch");
+}
+
+template <int NT>
+int launch_skinny(LinearParams& p, bool f32, int splits, cudaStream_t st) {
+    void (*kern)(LinearParams, int) = f32 ? skinny_kernel<NT, true> : skinny_kernel<NT, false>;
+    constexpr size_t smem = sizeof(SkinnySmem<NT>) + 1024;
+    static_assert(smem <= 232448, "shared memory budget");
+    static KernelInfo info[64][2];
+    static std::mutex mu;
+    int dev = 0;
+    OSM_TRY(current_device(&dev));
+    KernelInfo& ki = info[dev][f32 ? 1 : 0];
+    {
+        std::lock_guard<std::mutex> lk(mu);
+        if (!ki.ready) {
+            OSM_TRY(check_cuda(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                    static_cast<int>(smem)), "linear_hp smem attribute"));
+            ki.ready = true;
+        }
+    }
+    const int64_t mtiles = ceil_div(p.M, NT);
+    if (mtiles > 65535) return fail(OSM_ERR_UNSUPPORTED, "linear_hp: too many token tiles");
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(p.N, ROWS) * splits), static_cast<unsigned>(mtiles), 1);
+    cfg.blockDim = dim3(SK_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(splits);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = splits > 1 ? 2 : 1;
+    return check_cuda(cudaLaunchKernelEx(&cfg, kern, p, splits), "linear_hp launch");
+}
+
+}  // namespace
+
+int launch_linear_hp(const osm_plan* pl, const uint16_t* X, int64_t M, const uint16_t* w_hp, const float* bias, int act,
+                     const Onto& onto, void* Y, int y_dtype, cudaStream_t st) {
+    LinearParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.bias = bias;
+    p.Y = Y;
+    p.onto = onto;
+    p.status = pl->d_status;
+    p.wait_limit_ns = pl->wait_limit_ns;
+    p.M = M;
+    p.N = pl->N;
+    p.ksteps = static_cast<int>(pl->kp / KSTEP);
+    p.act = act;
+    const bool f32 = y_dtype == OSM_DT_F32;
+    const int64_t ntiles = ceil_div(pl->N, ROWS);
+    // Tokens per tile: the smallest width that takes them all, up to 256; from
+    // there on CTA pairs, once their tiles fill the GPU.
+    const int64_t pair_tiles = ceil_div(M, 256) * ceil_div(pl->N, PK_N);
+    const bool pair = M > 256 && pair_tiles >= 74;
+    int nt = M <= 16 ? 16 : (M <= 32 ? 32 : (M <= 64 ? 64 : 128));
+    // K is split until the CTAs cover the SMs, each rank keeping four K-steps or more.
+    int splits = 1;
+    const int64_t ctas = ntiles * ceil_div(M, nt);
+    while (splits < 8 && ctas * splits < 148 && p.ksteps / (2 * splits) >= 4) splits *= 2;
+    const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+    OSM_TRY(make_map(&p.tm_x, bf, X, pl->K, M, pl->K * 2, KSTEP, pair ? ROWS : nt, sw, "X"));
+    OSM_TRY(make_map(&p.tm_w, bf, w_hp, pl->kp, pl->N, pl->kp * 2, KSTEP, ROWS, sw, "w_hp"));
+    if (pair) return launch_pair(p, f32, pl->N * pl->kp * 2, st);
+    if (nt == 16) return launch_skinny<16>(p, f32, splits, st);
+    if (nt == 32) return launch_skinny<32>(p, f32, splits, st);
+    if (nt == 64) return launch_skinny<64>(p, f32, splits, st);
+    return launch_skinny<128>(p, f32, splits, st);
+}
+
+}  // namespace osm

@@ -17,6 +17,7 @@
 
 #include "osm_internal.h"
 #include "osm_mx.cuh"
+#include "osm_norm.cuh"
 #include "osm_ptx.cuh"
 
 namespace osm {
@@ -1060,6 +1061,85 @@ __global__ void __launch_bounds__(NT, (NT <= 256 ? 3 : 2)) quantize_act_pair_ker
     }
 }
 
+// ------------------------------------------------- norm, then quantize_act
+//
+// norm_quantize_act: h = bf16(norm of the row, modulated), then quantize_act
+// of h, without h ever leaving the SM. The statistics are those of
+// osm_norm.cuh, the rounding to BF16 and everything after it that of
+// quantize_act, so the operands are the ones that osm_norm_modulate followed
+// by osm_quantize_act write.
+
+// x' of a channel pair: bf16(bf16(n a + b) * inv_s).
+template <bool HPF>
+__device__ __forceinline__ uint32_t norm_smooth2(float2 x, float2 st, float2 a, float2 b, float2 sv, uint32_t f16mask) {
+    const float2 h = __ffma2_rn(norm::normalise(x, st), a, b);
+    const uint32_t w = mx::bf16x2_bits(h.x, h.y);
+    return HPF ? smooth2_mixed(w, sv, f16mask) : smooth2(w, sv);
+}
+
+// The form for every width: a CTA takes rows blockIdx.x, blockIdx.x +
+// gridDim.x, ...; each row is read twice (statistics, then values; the second
+// time from L1 or L2) and staged and encoded as in quantize_act_kernel.
+template <int MODE, bool F32>
+__global__ void __launch_bounds__(QA_THREADS) norm_quantize_kernel(QuantParams p, norm::Spec s, const void* X) {
+    constexpr bool HPF = MODE == QA_MX_F16;
+    ptx::grid_dep_launch();  // the dual_gemm that follows may start its prologue
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int nb = p.Kbp >> 5, nchunk = p.K / norm::CHUNK, nseg = (p.K + norm::SEG - 1) / norm::SEG;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    float2* part = reinterpret_cast<float2*>(smem);
+    uint8_t* sbuf = smem + ((nseg * 8 + 15) & ~15);
+    const bool center = s.kind == OSM_NORM_LAYER;
+    {
+        const int npb = p.Kbp - p.Kb, npad = npb + (p.kp - p.k);
+        for (int c = tid; c < npad; c += QA_THREADS) {
+            const int pos = p.Kb + c;
+            const int off = c < npb ? (pos >> 5) * QA_BLOCK_BYTES + (pos & 31) * 2
+                                    : nb * QA_BLOCK_BYTES + (p.k + c - npb) * 2;
+            *reinterpret_cast<uint16_t*>(sbuf + off) = 0;
+        }
+    }
+    for (int64_t t = blockIdx.x; t < p.M; t += gridDim.x) {
+        const size_t base = static_cast<size_t>(t) * p.K;
+        for (int seg = warp; seg < nseg; seg += QA_THREADS / 32) {
+            const int c = seg * 32 + lane;
+            float2 v[1][4];
+            const uint4 z = make_uint4(0, 0, 0, 0);
+            if constexpr (F32) {
+                const uint4* at = reinterpret_cast<const uint4*>(static_cast<const float*>(X) + base) + 2 * c;
+                norm::unpack(c < nchunk ? at[0] : z, c < nchunk ? at[1] : z, v[0]);
+            } else {
+                const uint4* at = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(X) + base) + c;
+                norm::unpack(c < nchunk ? at[0] : z, v[0]);
+            }
+            norm::segment_stats<1>(v, c < nchunk, center, norm::seg_cols(seg, p.K), lane, part + seg, 0);
+        }
+        __syncthreads();
+        float2 st[1];
+        norm::join_rows<1>(part, 0, nseg, p.K, center, s.eps, lane, st);
+        const int64_t mrow = s.scale || s.shift ? t / s.mod_rows : 0;
+        for (int c = tid; c < (p.K >> 1); c += QA_THREADS) {
+            float2 x, a, b;
+            if constexpr (F32) {
+                x = reinterpret_cast<const float2*>(static_cast<const float*>(X) + base)[c];
+            } else {
+                const uint32_t w = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(X) + base)[c];
+                x = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+            }
+            norm::coefficients(s, mrow, 2 * c, a, b);
+            const int2 dv = __ldg(reinterpret_cast<const int2*>(p.route) + c);
+            const uint32_t h = norm_smooth2<HPF>(x, st[0], a, b, __ldg(reinterpret_cast<const float2*>(p.inv_s) + c),
+                                                 HPF ? slot_mask(dv, nb * QA_BLOCK_BYTES) : 0u);
+            *reinterpret_cast<uint16_t*>(sbuf + dv.x) = static_cast<uint16_t>(h);
+            *reinterpret_cast<uint16_t*>(sbuf + dv.y) = static_cast<uint16_t>(h >> 16);
+        }
+        __syncthreads();  // staged row complete, statistics read
+        encode_staged<MODE>(p, ptx::smem_u32(sbuf), 0, static_cast<int>(t), 1);
+        if (t == p.M - 1) zero_padding_scale_rows(p);
+        __syncthreads();  // staged row free for the next one
+    }
+}
+
 template <int S>
 size_t pair_smem_bytes(int K, int nb, int kp) {
     return static_cast<size_t>(S) * 2 * K * 2 + ((qa_ip_bytes(nb, kp) + 7) & ~7) + 8 * S;
@@ -1226,15 +1306,44 @@ static int launch_pair(const QuantParams& p, int mode, cudaStream_t st) {
     return check_cuda(cudaGetLastError(), "quantize_act launch");
 }
 
-int launch_quantize_act(const osm_plan* pl, const uint16_t* X, int64_t M, uint8_t* codes,
-                        uint8_t* scales, uint16_t* hp, cudaStream_t st) {
-    if (M > 0x7FFFFFFF) return fail(OSM_ERR_UNSUPPORTED, "quantize_act: M too large");
-    QuantParams p{X, pl->d_inv_s, pl->d_route, static_cast<int>(M), static_cast<int>(pl->K),
+static QuantParams quant_params(const osm_plan* pl, const uint16_t* X, int64_t M, uint8_t* codes, uint8_t* scales,
+                                uint16_t* hp) {
+    return QuantParams{X, pl->d_inv_s, pl->d_route, static_cast<int>(M), static_cast<int>(pl->K),
                   static_cast<int>(pl->k), static_cast<int>(pl->Kb), static_cast<int>(pl->Kbp),
                   static_cast<int>(pl->kp), codes, scales, hp, pl->d_status, pl->wait_limit_ns,
                   (pl->debug_flags & OSM_DEBUG_STARVE_QUANTIZE) ? 16u : 0u, pl->hp_fp16,
                   static_cast<int>(pl->Kbp / (4 * block_elems(pl->fmt))), nvfp4_k(pl->g_act), pow2f(pl->g_act),
                   pow2f(-pl->g_act)};
+}
+
+int launch_norm_quantize(const osm_plan* pl, const void* X, int x_dtype, int64_t M, const osm_norm_spec* spec,
+                         uint8_t* codes, uint8_t* scales, uint16_t* hp, cudaStream_t st) {
+    const bool f32 = x_dtype == OSM_DT_F32;
+    const QuantParams p = quant_params(pl, f32 ? nullptr : static_cast<const uint16_t*>(X), M, codes, scales, hp);
+    const norm::Spec s{spec->kind, spec->eps, spec->weight, spec->bias, spec->scale, spec->shift,
+                       spec->mod_rows > 0 ? spec->mod_rows : 1, spec->mod_stride};
+    const int mode = pl->fmt == OSM_FMT_NVFP4 ? QA_NV : (pl->hp_fp16 ? QA_MX_F16 : QA_MX);
+    const int nseg = static_cast<int>(ceil_div(pl->K, norm::SEG));
+    const size_t smem = ((nseg * 8 + 15) & ~15) + qa_row_stride(static_cast<int>(pl->Kbp / 32), static_cast<int>(pl->kp));
+    auto pick = [&](auto f) {
+        constexpr bool F = decltype(f)::value;
+        return mode == QA_NV ? norm_quantize_kernel<QA_NV, F>
+                             : (mode == QA_MX_F16 ? norm_quantize_kernel<QA_MX_F16, F> : norm_quantize_kernel<QA_MX, F>);
+    };
+    auto kern = f32 ? pick(std::true_type{}) : pick(std::false_type{});
+    int per_sm = 0, sms = 0;
+    int rc = prepare_kernel(reinterpret_cast<const void*>(kern), QA_THREADS, smem, &per_sm, &sms);
+    if (rc) return rc;
+    if (per_sm < 1) return fail(OSM_ERR_UNSUPPORTED, "norm_quantize_act: no CTA fits (K = %lld)", (long long)pl->K);
+    const int64_t grid = M < static_cast<int64_t>(sms) * per_sm ? M : static_cast<int64_t>(sms) * per_sm;
+    kern<<<static_cast<unsigned>(grid), QA_THREADS, smem, st>>>(p, s, X);
+    return check_cuda(cudaGetLastError(), "norm_quantize_act launch");
+}
+
+int launch_quantize_act(const osm_plan* pl, const uint16_t* X, int64_t M, uint8_t* codes,
+                        uint8_t* scales, uint16_t* hp, cudaStream_t st) {
+    if (M > 0x7FFFFFFF) return fail(OSM_ERR_UNSUPPORTED, "quantize_act: M too large");
+    const QuantParams p = quant_params(pl, X, M, codes, scales, hp);
     const int mode = pl->fmt == OSM_FMT_NVFP4 ? QA_NV : (pl->hp_fp16 ? QA_MX_F16 : QA_MX);
     const int stride = qa_row_stride(static_cast<int>(pl->Kbp / 32), static_cast<int>(pl->kp));
     // streaming form: two CTAs of at most 110 KB per SM
