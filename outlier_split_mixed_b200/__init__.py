@@ -94,6 +94,8 @@ class OsmError(RuntimeError):
 def lib():
     """The loaded libosm (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -118,13 +120,18 @@ def _check(rc: int):
         raise OsmError(rc, last_error())
 
 
+_raw_stream = None  # torch's current stream of a device, as its address
+
+
 def _stream(stream):
+    global _raw_stream
     if stream is None:
-        import torch
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-    if isinstance(stream, int):
-        return ctypes.c_void_p(stream)
-    return ctypes.c_void_p(stream.cuda_stream)
+        if _raw_stream is None:
+            import torch
+            torch.cuda.init()
+            _raw_stream = (torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice)
+        return _raw_stream[0](_raw_stream[1]())
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _ptr(t, name, dtypes=None, numel=None, allow_none=False):
@@ -141,7 +148,7 @@ def _ptr(t, name, dtypes=None, numel=None, allow_none=False):
         raise ValueError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
     if numel is not None and t.numel() * t.element_size() < numel:
         raise ValueError(f"{name} holds {t.numel() * t.element_size()} bytes, needs {numel}")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _host_ptr(a: np.ndarray):
@@ -149,14 +156,21 @@ def _host_ptr(a: np.ndarray):
     return ctypes.c_void_p(a.ctypes.data)
 
 
+_types = {}
+
+
 def _bf16_types():
-    import torch
-    return (torch.bfloat16, torch.int16, torch.uint16)
+    if "bf16" not in _types:
+        import torch
+        _types["bf16"] = (torch.bfloat16, torch.int16, torch.uint16)
+    return _types["bf16"]
 
 
 def _u8_types():
-    import torch
-    return (torch.uint8,)
+    if "u8" not in _types:
+        import torch
+        _types["u8"] = (torch.uint8,)
+    return _types["u8"]
 
 
 # ----------------------------------------------------------------- plans
@@ -177,6 +191,7 @@ class Plan:
         _check(lib().osm_plan_create(K, N, k, _host_ptr(s), _host_ptr(O) if k else None, int(wscale_mode),
                                      ctypes.byref(h)))
         self._h = h
+        self._sizes = {}
         self.s, self.O, self.wscale_mode = s, O, int(wscale_mode)
         d = [ctypes.c_int64() for _ in range(6)]
         _check(lib().osm_plan_dims(self._h, *[ctypes.byref(x) for x in d]))
@@ -205,9 +220,15 @@ class Plan:
 
     def sizes(self, rows: int):
         """(codes_bytes, scales_bytes, hp_bytes) for `rows` rows."""
-        c, s, h = ctypes.c_size_t(), ctypes.c_size_t(), ctypes.c_size_t()
-        _check(lib().osm_plan_sizes(self._h, rows, ctypes.byref(c), ctypes.byref(s), ctypes.byref(h)))
-        return int(c.value), int(s.value), int(h.value)
+        key = (rows, self.fmt)
+        got = self._sizes.get(key)
+        if got is None:
+            c, s, h = ctypes.c_size_t(), ctypes.c_size_t(), ctypes.c_size_t()
+            _check(lib().osm_plan_sizes(self._h, rows, ctypes.byref(c), ctypes.byref(s), ctypes.byref(h)))
+            got = int(c.value), int(s.value), int(h.value)
+            if len(self._sizes) < 64:
+                self._sizes[key] = got
+        return got
 
     def status(self, clear: bool = True, stream=None) -> int:
         v = ctypes.c_uint32()
@@ -563,58 +584,64 @@ class _NormSpec(ctypes.Structure):
                 ("shift", _P), ("mod_rows", _I64), ("mod_stride", _I64)]
 
 
-def _here(t, name):
-    """`t` has to be on the current device: the kernels are launched there."""
-    import torch
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+def _device() -> int:
+    """The current device, where the kernels are launched."""
+    if _raw_stream is None:
+        _stream(None)
+    return _raw_stream[1]()
 
 
-def _operand(t, name, dtypes, shape, allow_none=False):
-    """Device pointer of a contiguous tensor of this shape on the current device."""
-    if t is None and allow_none:
-        return None
-    p = _ptr(t, name, dtypes)
-    _here(t, name)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, needs {tuple(shape)}")
-    return p
+def _operand(t, name, dtypes, shape, dev):
+    """Address of a contiguous tensor of this type and shape on device `dev`."""
+    if t.get_device() == dev and t.dtype in dtypes and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    _ptr(t, name, dtypes)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    raise ValueError(f"{name} has shape {tuple(t.shape)}, needs {tuple(shape)}")
+
+
+def _stream_types():
+    """The types a residual stream can have, with their DT_* codes."""
+    if "stream" not in _types:
+        import torch
+        _types["stream"] = {torch.bfloat16: DT_BF16, torch.float32: DT_F32}
+        _types["f32"], _types["bf16 alone"] = (torch.float32,), (torch.bfloat16,)
+    return _types["stream"]
 
 
 def _stream_type(t, name):
-    """DT_* of a residual stream tensor."""
-    import torch
-    if t.dtype == torch.float32:
-        return DT_F32
-    if t.dtype == torch.bfloat16:
-        return DT_BF16
-    raise ValueError(f"{name} has dtype {t.dtype}, expected torch.bfloat16 or torch.float32")
+    code = _stream_types().get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected torch.bfloat16 or torch.float32")
+    return code
 
 
-def _vector(t, name, D, allow_none=True):
-    import torch
-    return _operand(t, name, (torch.float32,), (D,), allow_none)
+def _vector(t, name, D, dev):
+    return None if t is None else _operand(t, name, _types["f32"], (D,), dev)
 
 
-def _shared_rows(t, name, M, D, rows):
-    """(pointer, rows, stride) of modulation or gate rows: [D] (one row), or [B][D] whose rows may lie apart (a
-    slice of a wider tensor); `rows` tokens share a row (default: M tokens in B equal parts)."""
-    import torch
+def _shared_rows(t, name, M, D, rows, dev):
+    """(address, rows, stride) of modulation or gate rows: [D] (one row), or [B][D] whose rows may lie apart (a slice
+    of a wider tensor); `rows` tokens share a row (default: M tokens in B equal parts)."""
     if t is None:
         return None, 1, 0
-    if t.dim() not in (1, 2) or t.dtype != torch.float32 or not t.is_cuda:
+    s = t.shape
+    if len(s) not in (1, 2) or t.dtype not in _types["f32"] or not t.is_cuda:
         raise ValueError(f"{name} must be a float32 CUDA tensor [D] or [B][D]")
-    _here(t, name)
-    B = 1 if t.dim() == 1 else t.shape[0]
-    if t.shape[-1] != D or t.stride(-1) != 1:
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    stride = t.stride()
+    if s[-1] != D or stride[-1] != 1:
         raise ValueError(f"{name} needs {D} contiguous columns")
+    B, step = (1, D) if len(s) == 1 else (s[0], stride[0])
     if rows is None:
         if B < 1 or M % B:
             raise ValueError(f"{name} has {B} rows for {M} tokens: say how many tokens share one")
         rows = M // B
     if rows < 1 or -(-M // rows) > B:
         raise ValueError(f"{name} has {B} rows, {M} tokens by {rows} need {-(-M // max(rows, 1))}")
-    return ctypes.c_void_p(t.data_ptr()), int(rows), int(t.stride(0)) if t.dim() == 2 else D
+    return t.data_ptr(), rows, step
 
 
 class Norm:
@@ -623,18 +650,27 @@ class Norm:
 
     def __init__(self, kind: int = NORM_LAYER, eps: float = 1e-6, weight=None, bias=None, scale=None, shift=None,
                  mod_rows: int | None = None):
-        self.kind, self.eps, self.weight, self.bias = int(kind), float(eps), weight, bias
+        self.kind, self.eps, self.weight, self.bias = kind, eps, weight, bias
         self.scale, self.shift, self.mod_rows = scale, shift, mod_rows
 
-    def spec(self, M: int, D: int) -> _NormSpec:
-        scale, rows, stride = _shared_rows(self.scale, "scale", M, D, self.mod_rows)
-        shift, rows2, stride2 = _shared_rows(self.shift, "shift", M, D, self.mod_rows)
+    def spec(self, M: int, D: int, dev: int | None = None) -> _NormSpec:
+        _stream_types()
+        if dev is None:
+            dev = self._any_device()
+        scale, rows, stride = _shared_rows(self.scale, "scale", M, D, self.mod_rows, dev)
+        shift, rows2, stride2 = _shared_rows(self.shift, "shift", M, D, self.mod_rows, dev)
         if self.scale is None:
             rows, stride = rows2, stride2
         elif self.shift is not None and (rows2 != rows or (rows < M and stride2 != stride)):
             raise ValueError("scale and shift must have the same rows and row stride")
-        return _NormSpec(self.kind, self.eps, _vector(self.weight, "weight", D), _vector(self.bias, "bias", D), scale,
-                         shift, rows, stride)
+        return _NormSpec(self.kind, self.eps, _vector(self.weight, "weight", D, dev), _vector(self.bias, "bias", D, dev),
+                         scale, shift, rows, stride)
+
+    def _any_device(self) -> int:
+        for t in (self.scale, self.shift, self.weight, self.bias):
+            if t is not None:
+                return t.get_device()
+        return -1
 
 
 def _new(shape, dtype, like, stream):
@@ -649,13 +685,17 @@ def _new(shape, dtype, like, stream):
 
 def norm_modulate(X, norm: Norm, out=None, stream=None):
     """H = bf16(norm(X)) (osm_norm_modulate). X: [M][D] BF16 or float32; out: [M][D] BF16 (may be X)."""
-    import torch
-    M, D = X.shape
-    dt = _stream_type(X, "X")
+    M, D = shape = X.shape
+    types = _stream_types()
+    _stream_type(X, "X")
+    _ptr(X, "X")
+    dev = _device()
+    bf = _types["bf16 alone"]
     if out is None:
-        out = _new((M, D), torch.bfloat16, X, stream)
-    _check(lib().osm_norm_modulate(_operand(X, "X", None, (M, D)), dt, M, D, ctypes.byref(norm.spec(M, D)),
-                                   _operand(out, "out", (torch.bfloat16,), (M, D)), _stream(stream)))
+        out = _new(shape, bf[0], X, stream)
+    _check(lib().osm_norm_modulate(_operand(X, "X", types, shape, dev), types[X.dtype], M, D,
+                                   ctypes.byref(norm.spec(M, D, dev)), _operand(out, "out", bf, shape, dev),
+                                   _stream(stream)))
     return out
 
 
@@ -663,56 +703,64 @@ def residual_norm(R, Y, gate=None, gate_rows: int | None = None, alpha: float = 
                   pre: Norm | None = None, out=None, h=None, stream=None):
     """(R + alpha * gate * post(Y), pre of it in BF16 or None) (osm_residual_norm). R: [M][D] BF16 or float32, Y: [M][D]
     BF16; out may be R, h may be Y."""
-    import torch
-    M, D = R.shape
-    dt = _stream_type(R, "R")
+    M, D = shape = R.shape
+    code = _stream_type(R, "R")
+    if pre is None and h is not None:
+        raise ValueError("h goes with pre")
+    _ptr(R, "R")
+    dev = _device()
+    own, bf = (R.dtype,), _types["bf16 alone"]
     if out is None:
-        out = _new((M, D), R.dtype, R, stream)
-    if pre is None:
-        if h is not None:
-            raise ValueError("h goes with pre")
-    elif h is None:
-        h = _new((M, D), torch.bfloat16, R, stream)
-    g, rows, stride = _shared_rows(gate, "gate", M, D, gate_rows)
-    bf = (torch.bfloat16,)
-    _check(lib().osm_residual_norm(_operand(R, "R", None, (M, D)), dt, _operand(Y, "Y", bf, (M, D)), M, D,
-                                   ctypes.byref(post.spec(M, D)) if post is not None else None, g, rows, stride,
-                                   float(alpha), ctypes.byref(pre.spec(M, D)) if pre is not None else None,
-                                   _operand(out, "out", (R.dtype,), (M, D)),
-                                   _operand(h, "h", bf, (M, D), allow_none=True), _stream(stream)))
+        out = _new(shape, R.dtype, R, stream)
+    if pre is not None and h is None:
+        h = _new(shape, bf[0], R, stream)
+    g, rows, stride = _shared_rows(gate, "gate", M, D, gate_rows, dev)
+    _check(lib().osm_residual_norm(_operand(R, "R", own, shape, dev), code, _operand(Y, "Y", bf, shape, dev), M, D,
+                                   None if post is None else ctypes.byref(post.spec(M, D, dev)), g, rows, stride, alpha,
+                                   None if pre is None else ctypes.byref(pre.spec(M, D, dev)),
+                                   _operand(out, "out", own, shape, dev),
+                                   None if h is None else _operand(h, "h", bf, shape, dev), _stream(stream)))
     return out, h
 
 
-def _packed_ptrs(plan: Plan, rows: int, codes, scales, hp, which: str):
-    cb, sb, hb = plan.sizes(rows)
-    for t, n in ((codes, "codes"), (scales, "scales"), (hp, "hp")):
-        if t is not None:
-            _here(t, f"{which}_{n}")
-    return (_ptr(codes, f"{which}_codes", _u8_types(), cb, allow_none=cb == 0),
-            _ptr(scales, f"{which}_scales", _u8_types(), sb, allow_none=sb == 0),
-            _ptr(hp, f"{which}_hp", _bf16_types(), hb, allow_none=hb == 0))
+def _packed_ptrs(plan: Plan, rows: int, codes, scales, hp, which: str, dev: int):
+    """Addresses of packed operands, with their sizes checked."""
+    got = []
+    for t, n, types, name in zip((codes, scales, hp), plan.sizes(rows), (_u8_types(), _u8_types(), _bf16_types()),
+                                 ("codes", "scales", "hp")):
+        if n == 0 and (t is None or t.numel() == 0):
+            got.append(None)
+            continue
+        p = _ptr(t, f"{which}_{name}", types, n)
+        if t.get_device() != dev:
+            raise ValueError(f"{which}_{name} is on {t.device}, the current device is cuda:{dev}")
+        got.append(p)
+    return got
 
 
 def norm_quantize_act(plan: Plan, X, norm: Norm, a_codes, a_scales, a_hp, stream=None):
     """quantize_act of norm_modulate(X) in one pass (osm_norm_quantize_act). X: [M][plan.K] BF16 or float32."""
-    M = X.shape[0]
-    _check(lib().osm_norm_quantize_act(plan.handle, _operand(X, "X", None, (M, plan.K)), _stream_type(X, "X"), M,
-                                       ctypes.byref(norm.spec(M, plan.K)),
-                                       *_packed_ptrs(plan, M, a_codes, a_scales, a_hp, "a"), _stream(stream)))
+    M, K = X.shape[0], plan.K
+    code = _stream_type(X, "X")
+    dev = _device()
+    _check(lib().osm_norm_quantize_act(plan.handle, _operand(X, "X", _types["stream"], (M, K), dev), code, M,
+                                       ctypes.byref(norm.spec(M, K, dev)),
+                                       *_packed_ptrs(plan, M, a_codes, a_scales, a_hp, "a", dev), _stream(stream)))
 
 
 def dual_gemm_residual(plan: Plan, a_codes, a_scales, a_hp, M: int, w_codes, w_scales, w_hp, R, out=None, bias=None,
                        gate=None, gate_rows: int | None = None, stream=None):
     """R + gate * (the dual-branch product + bias) (osm_dual_gemm_residual). R: [M][N] BF16 or float32; out may be R."""
     N = plan.N
-    dt = _stream_type(R, "R")
+    shape, code, own, dev = (M, N), _stream_type(R, "R"), (R.dtype,), _device()
     if out is None:
-        out = _new((M, N), R.dtype, R, stream)
-    g, rows, stride = _shared_rows(gate, "gate", M, N, gate_rows)
-    _check(lib().osm_dual_gemm_residual(plan.handle, *_packed_ptrs(plan, M, a_codes, a_scales, a_hp, "a"), M,
-                                        *_packed_ptrs(plan, N, w_codes, w_scales, w_hp, "w"),
-                                        _vector(bias, "bias", N), g, rows, stride, _operand(R, "R", None, (M, N)), dt,
-                                        _operand(out, "out", (R.dtype,), (M, N)), _stream(stream)))
+        out = _new(shape, R.dtype, R, stream)
+    g, rows, stride = _shared_rows(gate, "gate", M, N, gate_rows, dev)
+    _check(lib().osm_dual_gemm_residual(plan.handle, *_packed_ptrs(plan, M, a_codes, a_scales, a_hp, "a", dev), M,
+                                        *_packed_ptrs(plan, N, w_codes, w_scales, w_hp, "w", dev),
+                                        _vector(bias, "bias", N, dev), g, rows, stride,
+                                        _operand(R, "R", own, shape, dev), code, _operand(out, "out", own, shape, dev),
+                                        _stream(stream)))
     return out
 
 
@@ -726,20 +774,24 @@ def linear_hp(plan: Plan, X, w_hp, bias=None, act: int = ACT_NONE, gate=None, ga
     """[residual +] [gate *] act(X W + bias) in BF16 (osm_linear_hp). plan: hp_plan(K, N); X: [M][K] BF16; w_hp: packed
     by pack_weights; the output is BF16 or float32 (out's type, residual's, or dtype; BF16 by default). out may be
     residual."""
-    import torch
     M, N = X.shape[0], plan.N
+    shape, bf = (M, N), _bf16_types()
+    _stream_types()
     if out is None:
-        out = _new((M, N), residual.dtype if residual is not None else dtype or torch.bfloat16, X, stream)
+        out = _new(shape, residual.dtype if residual is not None else dtype or _types["bf16 alone"][0], X, stream)
     if dtype is not None and out.dtype != dtype:
         raise ValueError(f"the output has dtype {out.dtype}, dtype says {dtype}")
+    code, own, dev = _stream_type(out, "out"), (out.dtype,), _device()
     if M < 1:
         raise ValueError("X has no rows")
-    g, rows, stride = _shared_rows(gate, "gate", M, N, gate_rows)
-    _here(w_hp, "w_hp")
-    _check(lib().osm_linear_hp(plan.handle, _operand(X, "X", _bf16_types(), (M, plan.K)), M,
-                               _ptr(w_hp, "w_hp", _bf16_types(), plan.sizes(N)[2]), _vector(bias, "bias", N), int(act),
-                               g, rows, stride, _operand(residual, "residual", (out.dtype,), (M, N), allow_none=True),
-                               _operand(out, "out", None, (M, N)), _stream_type(out, "out"), _stream(stream)))
+    g, rows, stride = _shared_rows(gate, "gate", M, N, gate_rows, dev)
+    w = _ptr(w_hp, "w_hp", bf, plan.sizes(N)[2])
+    if w_hp.get_device() != dev:
+        raise ValueError(f"w_hp is on {w_hp.device}, the current device is cuda:{dev}")
+    _check(lib().osm_linear_hp(plan.handle, _operand(X, "X", bf, (M, plan.K), dev), M, w, _vector(bias, "bias", N, dev),
+                               act, g, rows, stride,
+                               None if residual is None else _operand(residual, "residual", own, shape, dev),
+                               _operand(out, "out", own, shape, dev), code, _stream(stream)))
     return out
 
 
@@ -747,17 +799,20 @@ def ffn_sublayer(up: Plan, down: Plan, R, norm: Norm, wu, wd, workspace, out=Non
                  gate_rows: int | None = None, stream=None):
     """R + gate * (FFN(norm(R)) + bias_down) (osm_ffn_sublayer): the weights and the workspace of ffn_block. R: [M][D]
     BF16 or float32; out may be R."""
-    M, D = R.shape
+    M, D = shape = R.shape
     if D != up.K:
         raise ValueError("R must have up.K columns")
+    code, own, dev = _stream_type(R, "R"), (R.dtype,), _device()
     if out is None:
-        out = _new((M, D), R.dtype, R, stream)
-    _here(workspace, "workspace")
-    g, rows, stride = _shared_rows(gate, "gate", M, D, gate_rows)
-    _check(lib().osm_ffn_sublayer(up.handle, down.handle, ctypes.byref(norm.spec(M, D)), _operand(R, "R", None, (M, D)),
-                                  _stream_type(R, "R"), M, *_packed_ptrs(up, up.N, *wu, "wu"),
-                                  *_packed_ptrs(down, down.N, *wd, "wd"), _vector(bias_down, "bias_down", down.N), g,
-                                  rows, stride, _operand(out, "out", (R.dtype,), (M, D)), _ptr(workspace, "workspace"),
+        out = _new(shape, R.dtype, R, stream)
+    if workspace.get_device() != dev:
+        raise ValueError(f"workspace is on {workspace.device}, the current device is cuda:{dev}")
+    g, rows, stride = _shared_rows(gate, "gate", M, D, gate_rows, dev)
+    _check(lib().osm_ffn_sublayer(up.handle, down.handle, ctypes.byref(norm.spec(M, D, dev)),
+                                  _operand(R, "R", own, shape, dev), code, M, *_packed_ptrs(up, up.N, *wu, "wu", dev),
+                                  *_packed_ptrs(down, down.N, *wd, "wd", dev),
+                                  _vector(bias_down, "bias_down", down.N, dev), g, rows, stride,
+                                  _operand(out, "out", own, shape, dev), _ptr(workspace, "workspace"),
                                   workspace.numel() * workspace.element_size(), _stream(stream)))
     return out
 

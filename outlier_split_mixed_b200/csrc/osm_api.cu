@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -46,12 +47,15 @@ float nvfp4_k(int g) { return std::ldexp(1.0f / 6.0f, -g); }
 int check_device() {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return fail(OSM_ERR_CUDA, "no CUDA device");
+    static std::atomic<uint64_t> good{0};  // devices that have passed
+    if (dev >= 0 && dev < 64 && (good.load(std::memory_order_relaxed) >> dev & 1)) return OSM_OK;
     int major = 0, minor = 0;
     cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
     cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
     if (major != 10 || minor != 0)
         return fail(OSM_ERR_UNSUPPORTED, "device %d is sm_%d%d; libosm kernels are built for sm_100a", dev,
                     major, minor);
+    if (dev >= 0 && dev < 64) good.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
     return OSM_OK;
 }
 

@@ -3,7 +3,7 @@
 //   norm_modulate   h = bf16((N(x) w + b) (1 + scale) + shift)
 //   residual_norm   r' = r + alpha gate P(y), h = N(r') modulated likewise
 // One pass over the rows: each row is read once, its statistics are joined
-// across the block (osm_norm.cuh), and the outputs are written from the same
+// across its warps (osm_norm.cuh), and the outputs are written from the same
 // registers.
 
 #include <cuda_bf16.h>
@@ -28,301 +28,312 @@ struct RowParams {
     const uint16_t* y;      // [M][D] BF16: the sublayer's output (residual_norm)
     void* r_out;            // [M][D] in x's type (residual_norm)
     uint16_t* h;            // [M][D] BF16, or NULL without a pre-norm
-    const float* gate;      // [rows / share][gate_stride] or NULL
+    const float* gate;      // gate rows, gate_stride floats apart, or NULL
     int64_t gate_stride;
     float alpha;
     Spec post, pre;         // kind -1: none
-    int64_t M, share;       // tokens that share a modulation (and gate) row
-    int64_t groups_per_share, groups;
-    int64_t gate_rows;
+    uint32_t M, share;      // tokens of a run: they share their modulation and gate rows
+    uint32_t pre_rows, gate_rows;  // tokens per modulation row and per gate row (at most M)
+    uint32_t tile_rows, tiles_per_run, tiles;  // row tiles of a run (rows_kernel)
     int D;
-    int stages;             // slots of the ring of incoming row groups; 0: rows are loaded directly
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
+// Loads of the rows: each byte is read once, so they bypass L1 (which serves
+// the coefficients).
+__device__ __forceinline__ uint4 ld_row(const uint4* p) {
     uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
     return v;
 }
 
-// Rows of group g: `rows` (may be <= 0 in a short last share) from `row0` on.
-struct Group {
-    int64_t row0, mrow;
-    int rows;
-};
-template <int R>
-__device__ __forceinline__ Group group_of(const RowParams& p, int64_t g) {
-    const int64_t s = g / p.groups_per_share;
-    const int64_t off = (g - s * p.groups_per_share) * R;
-    const int64_t len = min(p.share, p.M - s * p.share);
-    return {s * p.share + off, s, static_cast<int>(min(static_cast<int64_t>(R), len - off))};
+// h = n a + b of the pre-norm, and (y or its norm) a + b of the gated sum:
+// alpha, gate and the post-norm's affine part in one pair.
+__device__ __forceinline__ void post_coefficients(const RowParams& p, uint32_t row, int j, float2& a, float2& b) {
+    float2 g = make_float2(p.alpha, p.alpha);
+    if (p.gate)
+        g = __fmul2_rn(g, __ldg(reinterpret_cast<const float2*>(p.gate + (row / p.gate_rows) * p.gate_stride + j)));
+    a = g;
+    b = make_float2(0.0f, 0.0f);
+    if (p.post.weight) a = __fmul2_rn(g, __ldg(reinterpret_cast<const float2*>(p.post.weight + j)));
+    if (p.post.bias) b = __fmul2_rn(g, __ldg(reinterpret_cast<const float2*>(p.post.bias + j)));
 }
 
-// Persistent CTAs over groups of R rows. Thread t holds chunks t, t + T, ...
-// (V of them) of every row of the group. A thread's chunks come through its
-// own slots of a ring in shared memory (16-byte asynchronous copies, waited
-// for by the thread that reads them: no barrier, no spinning). With V == 1
-// the coefficients of the thread's eight columns stay in registers for all
-// rows that share a modulation row.
-template <bool F32, bool HAS_Y, int V, int R, int MAXT, int MINB>
-__global__ void __launch_bounds__(MAXT, MINB) norm_rows_kernel(const RowParams p) {
-    constexpr int XQ = F32 ? 2 : 1;              // 16-byte words of x per chunk
-    constexpr int NQ = XQ + (HAS_Y ? 1 : 0);     // words per chunk in the ring
+// One row by a team of `nw` warps: warp j of it holds the segments j, j + nw,
+// ... (NS of them at most) in registers, as they are in memory. total() adds
+// up one value per segment over the row (a barrier of the team and a buffer of
+// its own, in turn, per call); coef(which, c, a, b) gives chunk c's
+// coefficients (0: gated sum, 1: pre-norm).
+template <bool F32, bool HAS_Y, int NS, class Total, class Coef>
+__device__ __forceinline__ void one_row(const RowParams& p, uint32_t row, int j, int nw, int lane, float inv_d,
+                                        Total total, Coef coef) {
+    constexpr int XQ = F32 ? 2 : 1;  // 16-byte words of x per chunk
+    const int nchunk = p.D / norm::CHUNK;
+    const size_t base = static_cast<size_t>(row) * nchunk;
+    uint4 xq[NS][XQ], yq[HAS_Y ? NS : 1];
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int t = 0; t < NS; ++t) {
+        const int c = (j + t * nw) * 32 + lane;
+#pragma unroll
+        for (int q = 0; q < XQ; ++q)
+            xq[t][q] = c < nchunk ? ld_row(reinterpret_cast<const uint4*>(p.x) + (base + c) * XQ + q) : zero;
+        if constexpr (HAS_Y)
+            yq[t] = c < nchunk ? ld_row(reinterpret_cast<const uint4*>(p.y) + base + c) : zero;
+    }
+    auto x_of = [&](int t, float2 (&v)[4]) {
+        if constexpr (F32) norm::unpack(xq[t][0], xq[t][1], v);
+        else norm::unpack(xq[t][0], v);
+    };
+    // (mean, 1 / deviation) of the row whose chunks get(t, v) gives
+    auto statistics = [&](auto get, const Spec& s) -> float2 {
+        float part[NS];
+        float mean = 0.0f;
+        if (s.kind == OSM_NORM_LAYER) {
+#pragma unroll
+            for (int t = 0; t < NS; ++t) {
+                float2 v[4];
+                get(t, v);
+                part[t] = norm::chunk_sum(v);
+            }
+            mean = __fmul_rn(total(part), inv_d);
+        }
+#pragma unroll
+        for (int t = 0; t < NS; ++t) {
+            float2 v[4];
+            get(t, v);
+            part[t] = (j + t * nw) * 32 + lane < nchunk ? norm::chunk_m2(v, mean) : 0.0f;
+        }
+        return make_float2(mean, norm::inverse_deviation(total(part), inv_d, s.eps));
+    };
+    if constexpr (HAS_Y) {
+        float2 st = make_float2(0.0f, 1.0f);
+        if (p.post.kind >= 0) st = statistics([&](int t, float2 (&v)[4]) { norm::unpack(yq[t], v); }, p.post);
+#pragma unroll
+        for (int t = 0; t < NS; ++t) {
+            const int c = (j + t * nw) * 32 + lane;
+            if (c >= nchunk) continue;
+            float2 xv[4], yv[4], a[4], b[4];
+            x_of(t, xv);
+            norm::unpack(yq[t], yv);
+            coef(0, c, a, b);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (p.post.kind >= 0) yv[i] = norm::normalise(yv[i], st);
+                xv[i] = __fadd2_rn(xv[i], __ffma2_rn(yv[i], a[i], b[i]));
+            }
+            // rounded to the residual stream's type: the norm reads what is stored
+            if constexpr (F32) {
+                xq[t][0] = make_uint4(__float_as_uint(xv[0].x), __float_as_uint(xv[0].y), __float_as_uint(xv[1].x),
+                                      __float_as_uint(xv[1].y));
+                xq[t][1] = make_uint4(__float_as_uint(xv[2].x), __float_as_uint(xv[2].y), __float_as_uint(xv[3].x),
+                                      __float_as_uint(xv[3].y));
+            } else {
+                xq[t][0] = make_uint4(mx::bf16x2_bits(xv[0].x, xv[0].y), mx::bf16x2_bits(xv[1].x, xv[1].y),
+                                      mx::bf16x2_bits(xv[2].x, xv[2].y), mx::bf16x2_bits(xv[3].x, xv[3].y));
+            }
+#pragma unroll
+            for (int q = 0; q < XQ; ++q) reinterpret_cast<uint4*>(p.r_out)[(base + c) * XQ + q] = xq[t][q];
+        }
+        if (p.pre.kind < 0) return;
+    }
+    const float2 st = statistics(x_of, p.pre);
+#pragma unroll
+    for (int t = 0; t < NS; ++t) {
+        const int c = (j + t * nw) * 32 + lane;
+        if (c >= nchunk) continue;
+        float2 xv[4], a[4], b[4];
+        x_of(t, xv);
+        coef(1, c, a, b);
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 hv = __ffma2_rn(norm::normalise(xv[i], st), a[i], b[i]);
+            o[i] = mx::bf16x2_bits(hv.x, hv.y);
+        }
+        reinterpret_cast<uint4*>(p.h)[base + c] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+}
+
+// Many rows: a CTA of 16 warps takes a tile of rows of one run, teams of W
+// warps a row each. The run's coefficients are laid out once per tile in
+// shared memory (FP32, four 16-byte words of a chunk in arrays of their own:
+// conflict-free 128-bit reads), where all teams read them.
+constexpr int ROWS_THREADS = 512;
+
+template <bool F32, bool HAS_Y, int W, int NS, int MINB>
+__global__ void __launch_bounds__(ROWS_THREADS, MINB) rows_kernel(const __grid_constant__ RowParams p) {
+    constexpr int TEAMS = ROWS_THREADS / 32 / W;
     extern __shared__ __align__(16) uint8_t smem[];
-    const int T = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int D = p.D, nchunk = D / norm::CHUNK, nseg = (D + norm::SEG - 1) / norm::SEG;
-    const int nw = T >> 5;
-    float2* part = reinterpret_cast<float2*>(smem);                 // [2][R][nseg]
-    const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + ((2 * R * nseg * 8 + 15) & ~15);
-    const uint32_t slot_bytes = static_cast<uint32_t>(R) * NQ * V * T * 16;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int team = warp / W, j = warp % W;
+    const int nchunk = p.D / norm::CHUNK, nseg = (p.D + norm::SEG - 1) / norm::SEG;
+    const float inv_d = __frcp_rn(static_cast<float>(p.D));
+    float* part = reinterpret_cast<float*>(smem) + team * 2 * W * NS;  // [2][W * NS]
+    float4* table = reinterpret_cast<float4*>(smem + TEAMS * 2 * W * NS * 4);
+    const int ntab = (HAS_Y ? 4 : 0) + (p.pre.kind >= 0 ? 4 : 0);  // arrays of nchunk words
     int flip = 0;
-
-    auto slot_addr = [&](int slot, int r, int q, int v) -> uint32_t {
-        return ring + slot * slot_bytes + ((((r * NQ) + q) * V + v) * T + tid) * 16;
-    };
-    auto x_ptr = [&](int64_t row, int c, int q) -> const uint4* {
-        return reinterpret_cast<const uint4*>(p.x) + (row * nchunk + c) * XQ + q;
-    };
-    auto y_ptr = [&](int64_t row, int c) -> const uint4* { return reinterpret_cast<const uint4*>(p.y) + row * nchunk + c; };
-    auto fetch = [&](int64_t g, int slot) {
-        if (g < p.groups) {
-            const Group gr = group_of<R>(p, g);
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                if (r < gr.rows)
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        const int c = tid + v * T;
-                        if (c < nchunk) {
-#pragma unroll
-                            for (int q = 0; q < XQ; ++q) cp_async16(slot_addr(slot, r, q, v), x_ptr(gr.row0 + r, c, q));
-                            if constexpr (HAS_Y) cp_async16(slot_addr(slot, r, XQ, v), y_ptr(gr.row0 + r, c));
-                        }
-                    }
-        }
-        cp_async_commit();
-    };
-
-    // Statistics of R rows whose values the accessor get(r, v, out) gives:
-    // one barrier; two copies of `part` so that the next call's writes need none.
-    auto statistics = [&](auto get, const Spec& s, float2 (&st)[R]) {
-        const bool center = s.kind == OSM_NORM_LAYER;
-        float2* pt = part + flip * R * nseg;
+    auto total = [&](const float (&v)[NS]) -> float {
+        float* at = part + flip * W * NS;
         flip ^= 1;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int seg = warp + v * nw;
-            if (seg < nseg) {
-                float2 val[R][4];
-#pragma unroll
-                for (int r = 0; r < R; ++r) get(r, v, val[r]);
-                norm::segment_stats<R>(val, tid + v * T < nchunk, center, norm::seg_cols(seg, D), lane, pt + seg, nseg);
-            }
-        }
-        __syncthreads();
-        norm::join_rows<R>(pt, nseg, nseg, D, center, s.eps, lane, st);
+        norm::warp_totals<NS>(v, lane, at + j, W);
+        if constexpr (W == 1) __syncwarp();
+        else asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(32 * W) : "memory");
+        return norm::join_total(at, nseg, lane);
     };
-
-    // coefficients: pre a, b; post (or the bare gate) ga, gb
-    float2 ca[V == 1 ? 4 : 1], cb[V == 1 ? 4 : 1], ga[V == 1 ? 4 : 1], gb[V == 1 ? 4 : 1];
-    auto pre_coef = [&](int64_t mrow, int j, float2& a, float2& b) { norm::coefficients(p.pre, mrow, j, a, b); };
-    auto post_coef = [&](int64_t grow, int j, float2& a, float2& b) {
-        float2 g = make_float2(p.alpha, p.alpha);
-        if (p.gate) g = __fmul2_rn(g, __ldg(reinterpret_cast<const float2*>(p.gate + grow * p.gate_stride + j)));
-        a = g;
-        b = make_float2(0.0f, 0.0f);
-        if (p.post.weight) a = __fmul2_rn(g, __ldg(reinterpret_cast<const float2*>(p.post.weight + j)));
-        if (p.post.bias) b = __fmul2_rn(g, __ldg(reinterpret_cast<const float2*>(p.post.bias + j)));
+    auto coef = [&](int which, int c, float2 (&a)[4], float2 (&b)[4]) {
+        const float4* at = table + (HAS_Y && which ? 4 : 0) * nchunk + c;
+        const float4 a0 = at[0], a1 = at[nchunk], b0 = at[2 * nchunk], b1 = at[3 * nchunk];
+        a[0] = make_float2(a0.x, a0.y);
+        a[1] = make_float2(a0.z, a0.w);
+        a[2] = make_float2(a1.x, a1.y);
+        a[3] = make_float2(a1.z, a1.w);
+        b[0] = make_float2(b0.x, b0.y);
+        b[1] = make_float2(b0.z, b0.w);
+        b[2] = make_float2(b1.x, b1.y);
+        b[3] = make_float2(b1.z, b1.w);
     };
-    int64_t held = -1;
-
-    if (p.stages)
-        for (int s = 0; s < p.stages - 1; ++s) fetch(blockIdx.x + static_cast<int64_t>(s) * gridDim.x, s);
-    int slot = 0;
-    for (int64_t g = blockIdx.x; g < p.groups; g += gridDim.x) {
-        const Group gr = group_of<R>(p, g);
-        uint4 xq[R][V][XQ], yq[HAS_Y ? R : 1][HAS_Y ? V : 1];
-        if (p.stages) {
-            int ahead = slot + p.stages - 1;
-            if (ahead >= p.stages) ahead -= p.stages;
-            fetch(g + static_cast<int64_t>(p.stages - 1) * gridDim.x, ahead);
-            if (p.stages == 4) cp_async_wait<3>();
-            else if (p.stages == 3) cp_async_wait<2>();
-            else cp_async_wait<1>();
-        }
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int c = tid + v * T;
-                const bool on = r < gr.rows && c < nchunk;
-#pragma unroll
-                for (int q = 0; q < XQ; ++q)
-                    xq[r][v][q] = !on ? make_uint4(0, 0, 0, 0)
-                                      : (p.stages ? lds128(slot_addr(slot, r, q, v)) : *x_ptr(gr.row0 + r, c, q));
-                if constexpr (HAS_Y)
-                    yq[r][v] = !on ? make_uint4(0, 0, 0, 0)
-                                   : (p.stages ? lds128(slot_addr(slot, r, XQ, v)) : *y_ptr(gr.row0 + r, c));
-            }
-        if (++slot >= p.stages) slot = 0;
-        if constexpr (V == 1) {
-            if (held != gr.mrow) {
-                held = gr.mrow;
-                const int j = tid * norm::CHUNK;
-                if (tid < nchunk)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (p.pre.kind >= 0) pre_coef(p.pre.scale || p.pre.shift ? gr.row0 / p.pre.mod_rows : 0, j + 2 * i, ca[i], cb[i]);
-                        if constexpr (HAS_Y) post_coef(p.gate ? gr.row0 / p.gate_rows : 0, j + 2 * i, ga[i], gb[i]);
-                    }
-            }
-        }
-        auto x_get = [&](int r, int v, float2 (&o)[4]) {
-            if constexpr (F32) norm::unpack(xq[r][v][0], xq[r][v][1], o);
-            else norm::unpack(xq[r][v][0], o);
-        };
-        if constexpr (HAS_Y) {
-            float2 st[R];
-            if (p.post.kind >= 0)
-                statistics([&](int r, int v, float2 (&o)[4]) { norm::unpack(yq[r][v], o); }, p.post, st);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int c = tid + v * T;
-                if (c >= nchunk) continue;
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    if (r >= gr.rows) continue;
-                    float2 xv[4], yv[4];
-                    x_get(r, v, xv);
-                    norm::unpack(yq[r][v], yv);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float2 a, b;
-                        if constexpr (V == 1) {
-                            a = ga[i];
-                            b = gb[i];
-                        } else {
-                            post_coef(p.gate ? gr.row0 / p.gate_rows : 0, c * norm::CHUNK + 2 * i, a, b);
-                        }
-                        if (p.post.kind >= 0) yv[i] = norm::normalise(yv[i], st[r]);
-                        xv[i] = __fadd2_rn(xv[i], __ffma2_rn(yv[i], a, b));
-                    }
-                    // rounded to the residual stream's type: the norm reads what is stored
-                    if constexpr (F32) {
-                        xq[r][v][0] = make_uint4(__float_as_uint(xv[0].x), __float_as_uint(xv[0].y),
-                                                 __float_as_uint(xv[1].x), __float_as_uint(xv[1].y));
-                        xq[r][v][1] = make_uint4(__float_as_uint(xv[2].x), __float_as_uint(xv[2].y),
-                                                 __float_as_uint(xv[3].x), __float_as_uint(xv[3].y));
-                    } else {
-                        xq[r][v][0] = make_uint4(mx::bf16x2_bits(xv[0].x, xv[0].y), mx::bf16x2_bits(xv[1].x, xv[1].y),
-                                                 mx::bf16x2_bits(xv[2].x, xv[2].y), mx::bf16x2_bits(xv[3].x, xv[3].y));
-                    }
-                    uint4* dst = reinterpret_cast<uint4*>(p.r_out) + ((gr.row0 + r) * nchunk + c) * XQ;
-#pragma unroll
-                    for (int q = 0; q < XQ; ++q) dst[q] = xq[r][v][q];
+    uint32_t held = 0xffffffffu;
+    for (uint32_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
+        const uint32_t run = tile / p.tiles_per_run;
+        const uint32_t first = run * p.share;
+        const uint32_t row0 = first + (tile - run * p.tiles_per_run) * p.tile_rows;
+        const uint32_t end = min(min(row0 + p.tile_rows, first + p.share), p.M);
+        if (held != run) {
+            if (held != 0xffffffffu) __syncthreads();  // the rows of the last run are done
+            held = run;
+            // word w of chunk c: columns 8c + 4 (w & 1) .. + 3 of a (w < 2) or b
+            for (int i = threadIdx.x; i < ntab / 2 * nchunk; i += ROWS_THREADS) {
+                const int k = i / nchunk, c = i - k * nchunk;  // k: table * 2 + half
+                const int col = c * norm::CHUNK + 4 * (k & 1);
+                float2 a0, a1, b0, b1;
+                if (HAS_Y && k < 2) {
+                    post_coefficients(p, first, col, a0, b0);
+                    post_coefficients(p, first, col + 2, a1, b1);
+                } else {
+                    norm::coefficients(p.pre, first / p.pre_rows, col, a0, b0);
+                    norm::coefficients(p.pre, first / p.pre_rows, col + 2, a1, b1);
                 }
+                float4* at = table + ((k >> 1) * 4 + (k & 1)) * nchunk + c;
+                at[0] = make_float4(a0.x, a0.y, a1.x, a1.y);
+                at[2 * nchunk] = make_float4(b0.x, b0.y, b1.x, b1.y);
             }
+            __syncthreads();
         }
-        if (!HAS_Y || p.pre.kind >= 0) {
-            float2 st[R];
-            statistics(x_get, p.pre, st);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int c = tid + v * T;
-                if (c >= nchunk) continue;
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    if (r >= gr.rows) continue;
-                    float2 xv[4];
-                    x_get(r, v, xv);
-                    uint32_t o[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float2 a, b;
-                        if constexpr (V == 1) {
-                            a = ca[i];
-                            b = cb[i];
-                        } else {
-                            pre_coef(p.pre.scale || p.pre.shift ? gr.row0 / p.pre.mod_rows : 0, c * norm::CHUNK + 2 * i, a, b);
-                        }
-                        const float2 hv = __ffma2_rn(norm::normalise(xv[i], st[r]), a, b);
-                        o[i] = mx::bf16x2_bits(hv.x, hv.y);
-                    }
-                    reinterpret_cast<uint4*>(p.h)[(gr.row0 + r) * nchunk + c] = make_uint4(o[0], o[1], o[2], o[3]);
-                }
-            }
-        }
+        for (uint32_t row = row0 + team; row < end; row += TEAMS)
+            one_row<F32, HAS_Y, NS>(p, row, j, W, lane, inv_d, total, coef);
     }
-    if (p.stages) cp_async_wait<0>();
 }
 
-template <bool F32, bool HAS_Y, int V, int R, int MAXT, int MINB>
-int launch_rows(RowParams p, cudaStream_t st) {
-    auto kern = norm_rows_kernel<F32, HAS_Y, V, R, MAXT, MINB>;
-    const int nchunk = p.D / norm::CHUNK, nseg = static_cast<int>(ceil_div(p.D, norm::SEG));
-    const int T = static_cast<int>(round_up(ceil_div(nchunk, V), 32));
-    const size_t head = (static_cast<size_t>(2) * R * nseg * 8 + 15) & ~size_t(15);
-    const size_t slot = static_cast<size_t>(R) * ((F32 ? 2 : 1) + (HAS_Y ? 1 : 0)) * V * T * 16;
-    const size_t budget = MINB >= 2 ? 110 * 1024 : 220 * 1024;
-    p.stages = head + 4 * slot <= budget ? 4 : (head + 3 * slot <= budget ? 3 : (head + 2 * slot <= budget ? 2 : 0));
-    const size_t smem = head + p.stages * slot;
-    p.groups_per_share = ceil_div(std::min(p.share, p.M), R);
-    p.groups = ceil_div(p.M, p.share) * p.groups_per_share;
-    // shared-memory limit, CTAs per SM and SM count: looked up once per device and shape
-    struct Setup {
-        size_t smem_set = 0;
-        std::map<std::pair<size_t, int>, int> per_sm;
-        int sms = 0;
+// Few rows, very wide ones, or a modulation row for each token: a CTA of as
+// many warps as the row has segments (16 at most) takes one row at a time and
+// reads its coefficients from global memory.
+template <bool F32, bool HAS_Y, int NS, int MINB>
+__global__ void __launch_bounds__(512, MINB) row_kernel(const __grid_constant__ RowParams p) {
+    __shared__ float part[2][16 * NS];
+    const int lane = threadIdx.x & 31, j = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    const int nseg = (p.D + norm::SEG - 1) / norm::SEG;
+    const float inv_d = __frcp_rn(static_cast<float>(p.D));
+    int flip = 0;
+    auto total = [&](const float (&v)[NS]) -> float {
+        float* at = part[flip];
+        flip ^= 1;
+        norm::warp_totals<NS>(v, lane, at + j, nw);
+        __syncthreads();
+        return norm::join_total(at, nseg, lane);
     };
-    static std::mutex mu;
-    static Setup cache[64];
-    int dev = 0, per_sm = 0, sms = 0;
-    int rc = check_cuda(cudaGetDevice(&dev), "cudaGetDevice");
-    if (rc) return rc;
-    if (dev < 0 || dev >= 64) return fail(OSM_ERR_UNSUPPORTED, "device index %d", dev);
-    {
-        std::lock_guard<std::mutex> lk(mu);
-        Setup& su = cache[dev];
-        if (smem > 48 * 1024 && su.smem_set < smem) {
-            if ((rc = check_cuda(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                      static_cast<int>(smem)), "norm smem attribute")))
-                return rc;
-            su.smem_set = smem;
-        }
-        auto it = su.per_sm.find({smem, T});
-        if (it == su.per_sm.end()) {
-            int n = 0;
-            if ((rc = check_cuda(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, T, smem), "norm occupancy")))
-                return rc;
-            it = su.per_sm.emplace(std::make_pair(smem, T), n).first;
-        }
-        per_sm = it->second;
-        if (!su.sms &&
-            (rc = check_cuda(cudaDeviceGetAttribute(&su.sms, cudaDevAttrMultiProcessorCount, dev), "SM count")))
-            return rc;
-        sms = su.sms;
+    for (uint64_t row = blockIdx.x; row < p.M; row += gridDim.x) {
+        const uint32_t r = static_cast<uint32_t>(row);
+        auto coef = [&](int which, int c, float2 (&a)[4], float2 (&b)[4]) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (HAS_Y && which == 0) post_coefficients(p, r, c * norm::CHUNK + 2 * i, a[i], b[i]);
+                else norm::coefficients(p.pre, r / p.pre_rows, c * norm::CHUNK + 2 * i, a[i], b[i]);
+            }
+        };
+        one_row<F32, HAS_Y, NS>(p, r, j, nw, lane, inv_d, total, coef);
     }
-    if (per_sm < 1) return fail(OSM_ERR_UNSUPPORTED, "norm: no CTA fits (D = %d)", p.D);
-    const int64_t grid = std::min<int64_t>(p.groups, static_cast<int64_t>(sms) * per_sm);
-    kern<<<static_cast<unsigned>(grid), T, smem, st>>>(p);
+}
+
+// Device, SM count and CTAs per SM of a kernel, looked up once per device,
+// CTA and shared-memory size.
+struct Setup {
+    std::mutex mu;
+    size_t smem_set[64] = {};
+    std::map<std::pair<size_t, int>, int> per_sm[64];
+};
+int prepare(Setup& su, const void* kern, int threads, size_t smem, int* ctas) {
+    static int sms[64] = {};
+    int dev = 0, rc;
+    if ((rc = check_cuda(cudaGetDevice(&dev), "cudaGetDevice"))) return rc;
+    if (dev < 0 || dev >= 64) return fail(OSM_ERR_UNSUPPORTED, "device index %d", dev);
+    std::lock_guard<std::mutex> lk(su.mu);
+    if (smem > 48 * 1024 && su.smem_set[dev] < smem) {
+        if ((rc = check_cuda(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                  static_cast<int>(smem)), "norm smem attribute")))
+            return rc;
+        su.smem_set[dev] = smem;
+    }
+    auto it = su.per_sm[dev].find({smem, threads});
+    if (it == su.per_sm[dev].end()) {
+        int n = 0;
+        if ((rc = check_cuda(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, smem), "norm occupancy")))
+            return rc;
+        if (n < 1) return fail(OSM_ERR_UNSUPPORTED, "norm: no CTA fits");
+        int s = 0;
+        if ((rc = check_cuda(cudaDeviceGetAttribute(&s, cudaDevAttrMultiProcessorCount, dev), "SM count"))) return rc;
+        sms[dev] = s;
+        it = su.per_sm[dev].emplace(std::make_pair(smem, threads), n).first;
+    }
+    *ctas = it->second * sms[dev];
+    return OSM_OK;
+}
+
+template <bool F32, bool HAS_Y, int W, int NS, int MINB>
+int launch_tiles(RowParams p, cudaStream_t st) {
+    static Setup su;
+    auto kern = rows_kernel<F32, HAS_Y, W, NS, MINB>;
+    const size_t smem = ROWS_THREADS / 32 / W * 2 * W * NS * 4 +
+                        static_cast<size_t>((HAS_Y ? 4 : 0) + (p.pre.kind >= 0 ? 4 : 0)) * (p.D / norm::CHUNK) * 16;
+    int ctas = 0;
+    OSM_TRY(prepare(su, reinterpret_cast<const void*>(kern), ROWS_THREADS, smem, &ctas));
+    // one tile per CTA: each run is cut into its part of them
+    const int64_t cuts = std::max<int64_t>(1, static_cast<int64_t>(ctas) * p.share / p.M);
+    p.tile_rows = static_cast<uint32_t>(ceil_div(p.share, cuts));
+    p.tiles_per_run = static_cast<uint32_t>(ceil_div(p.share, p.tile_rows));
+    p.tiles = static_cast<uint32_t>(ceil_div(p.M, p.share)) * p.tiles_per_run;
+    kern<<<std::min<uint32_t>(p.tiles, ctas), ROWS_THREADS, smem, st>>>(p);
+    return check_cuda(cudaGetLastError(), "norm launch");
+}
+
+template <bool F32, bool HAS_Y, int NS, int MINB>
+int launch_single(const RowParams& p, cudaStream_t st) {
+    static Setup su;
+    auto kern = row_kernel<F32, HAS_Y, NS, MINB>;
+    const int threads = 32 * static_cast<int>(std::min<int64_t>(16, ceil_div(p.D, norm::SEG)));
+    int ctas = 0;
+    OSM_TRY(prepare(su, reinterpret_cast<const void*>(kern), threads, 0, &ctas));
+    kern<<<std::min<uint32_t>(p.M, ctas), threads, 0, st>>>(p);
     return check_cuda(cudaGetLastError(), "norm launch");
 }
 
 template <bool F32, bool HAS_Y>
-int launch_width(const RowParams& p, bool grouped, cudaStream_t st) {
-    if (p.D <= 5120) {
-        if (grouped) return launch_rows<F32, HAS_Y, 1, 2, 640, HAS_Y ? 1 : 2>(p, st);
-        return launch_rows<F32, HAS_Y, 1, 1, 640, HAS_Y ? 1 : 2>(p, st);
+int launch_width(const RowParams& p, cudaStream_t st) {
+    // Tiles pay once a CTA has a row for each of its 16 warps (M from about
+    // 2400 rows on) and runs long enough to lay out their coefficients once.
+    const bool tiles = p.M >= 148 * 16 && p.share >= 64 && p.D <= 8192;
+    if (!tiles) {
+        if (p.D <= 8192) return launch_single<F32, HAS_Y, 2, 2>(p, st);
+        return launch_single<F32, HAS_Y, 16, 1>(p, st);
     }
-    if (p.D <= 10240) return launch_rows<F32, HAS_Y, 2, 1, 640, 1>(p, st);
-    if (p.D <= 20480) return launch_rows<F32, HAS_Y, 4, 1, 640, 1>(p, st);
-    return launch_rows<F32, HAS_Y, 8, 1, 1024, 1>(p, st);
+    if (p.D <= 512) return launch_tiles<F32, HAS_Y, 1, 2, 2>(p, st);
+    if (p.D <= 2048) return launch_tiles<F32, HAS_Y, 1, 8, 1>(p, st);
+    // warps per row: the row's words of a lane stay within its 128 registers
+    constexpr int W = F32 ? (HAS_Y ? 4 : 2) : (HAS_Y ? 2 : 1);
+    if (p.D <= 5120) return launch_tiles<F32, HAS_Y, W, 20 / W, 1>(p, st);
+    constexpr int V = F32 || HAS_Y ? 4 : 2;
+    return launch_tiles<F32, HAS_Y, V, 32 / V, 1>(p, st);
 }
 
 Spec to_spec(const osm_norm_spec* s) {
@@ -341,22 +352,22 @@ int launch_norm_rows(const void* X, int x_dtype, int64_t M, int64_t D, const uin
     p.r_out = R_out;
     p.h = H;
     p.gate = gate;
-    p.gate_rows = gate_rows > 0 ? gate_rows : 1;
     p.gate_stride = gate_stride;
     p.alpha = alpha;
     p.post = to_spec(post);
     p.pre = to_spec(pre);
-    p.M = M;
+    p.M = static_cast<uint32_t>(M);
     p.D = static_cast<int>(D);
-    // Rows are grouped inside the runs of tokens that share their modulation
-    // and gate rows; with two runs of different length, or none longer than a
-    // token, each row is a group of its own.
+    // A run of tokens shares its modulation and its gate row; with two runs of
+    // different length each row is a run of its own. M < 2^31 and a tile has at
+    // most M rows, so row numbers past the end fit 32 bits.
     const int64_t a = pre && (pre->scale || pre->shift) ? std::min(M, pre->mod_rows) : M;
     const int64_t b = gate ? std::min(M, gate_rows) : M;
-    p.share = a == M ? b : (b == M || a == b ? a : 1);
-    const bool grouped = p.share >= 2 && M >= 2 * 148;
-    if (Y) return x_dtype == OSM_DT_F32 ? launch_width<true, true>(p, grouped, st) : launch_width<false, true>(p, grouped, st);
-    return x_dtype == OSM_DT_F32 ? launch_width<true, false>(p, grouped, st) : launch_width<false, false>(p, grouped, st);
+    p.pre_rows = static_cast<uint32_t>(a);
+    p.gate_rows = static_cast<uint32_t>(b);
+    p.share = static_cast<uint32_t>(a == M ? b : (b == M || a == b ? a : 1));
+    if (Y) return x_dtype == OSM_DT_F32 ? launch_width<true, true>(p, st) : launch_width<false, true>(p, st);
+    return x_dtype == OSM_DT_F32 ? launch_width<true, false>(p, st) : launch_width<false, false>(p, st);
 }
 
 }  // namespace osm

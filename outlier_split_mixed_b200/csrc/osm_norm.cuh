@@ -2,15 +2,13 @@
 // (norm_modulate, residual_norm, norm_quantize_act).
 //
 // A row of D values is cut into chunks of 8 consecutive columns and segments
-// of 32 chunks (256 columns): one lane per chunk, one warp per segment. Each
-// segment gives its mean and the sum of squared deviations from that mean,
-// and the segments are joined by
-//     mean = sum n_s mean_s / D,   M2 = sum M2_s + n_s (mean_s - mean)^2,
-// so that the variance never comes from the difference of two large sums and
-// the row needs one block barrier. Every addition has a fixed place in the
-// tree (lanes joined at distances 1, 2, 4, 8, 16; segments in eight strided
-// parts), which does not depend on how a kernel maps segments to warps or
-// rows to lanes: all kernels get the same bits for the same row.
+// of 32 chunks (256 columns). A sum over the row is a fixed tree: the eight
+// values of a chunk, the 32 chunks of a segment (lanes at distances 1, 2, 4,
+// 8, 16), 16 segments (distances 1, 2, 4, 8), then the groups of 16 segments
+// in order. The tree does not depend on how a kernel maps rows and segments
+// to warps, so every kernel gets the same bits for the same row. The variance
+// is the sum of squared deviations from the row's mean, never a difference
+// of sums.
 #pragma once
 
 #include <cstdint>
@@ -65,111 +63,64 @@ __device__ __forceinline__ float chunk_m2(const float2 (&v)[4], float mean) {
     return __fadd_rn(s.x, s.y);
 }
 
-// Sums over the 32 lanes of R values per lane (R = 1, 2 or 4); every lane
-// gets all R. With more than one value the first steps halve the values a
-// lane carries instead of repeating the exchange for each of them.
-template <int R>
-__device__ __forceinline__ void warp_sums(float (&s)[R], int lane) {
-    if constexpr (R == 1) {
+// Totals over the warp of N values per lane, part[i * step] = the total of
+// s[i]: four at a time, the first two steps halving the values that a lane
+// carries (6 exchanges for four totals instead of 20).
+template <int N>
+__device__ __forceinline__ void warp_totals(const float (&s)[N], int lane, float* part, int step) {
+    const bool b0 = lane & 1, b1 = lane & 2;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) s[0] = __fadd_rn(s[0], __shfl_xor_sync(0xffffffffu, s[0], o));
-    } else if constexpr (R == 2) {
-        // lane bit 0 = row kept
-        const bool odd = lane & 1;
-        float k = odd ? s[1] : s[0];
-        k = __fadd_rn(k, __shfl_xor_sync(0xffffffffu, odd ? s[0] : s[1], 1));
-#pragma unroll
-        for (int o = 2; o < 32; o <<= 1) k = __fadd_rn(k, __shfl_xor_sync(0xffffffffu, k, o));
-        const float other = __shfl_xor_sync(0xffffffffu, k, 1);
-        s[0] = odd ? other : k;
-        s[1] = odd ? k : other;
-    } else {
-        static_assert(R == 4, "1, 2 or 4 rows");
-        const bool b0 = lane & 1, b1 = lane & 2;
-        // lane bit 0 selects rows {0, 1} or {2, 3}, bit 1 the row of the two
-        float k0 = b0 ? s[2] : s[0], k1 = b0 ? s[3] : s[1];
-        k0 = __fadd_rn(k0, __shfl_xor_sync(0xffffffffu, b0 ? s[0] : s[2], 1));
-        k1 = __fadd_rn(k1, __shfl_xor_sync(0xffffffffu, b0 ? s[1] : s[3], 1));
-        float k = b1 ? k1 : k0;
-        k = __fadd_rn(k, __shfl_xor_sync(0xffffffffu, b1 ? k0 : k1, 2));
+    for (int i = 0; i < N; i += 4) {
+        const float v0 = s[i], v1 = i + 1 < N ? s[i + 1] : 0.0f, v2 = i + 2 < N ? s[i + 2] : 0.0f,
+                    v3 = i + 3 < N ? s[i + 3] : 0.0f;
+        float k;
+        if (i + 1 < N) {
+            // lane bit 0 keeps {v0, v1} or {v2, v3}, bit 1 one of the two
+            float k0 = b0 ? v2 : v0, k1 = b0 ? v3 : v1;
+            k0 = __fadd_rn(k0, __shfl_xor_sync(0xffffffffu, b0 ? v0 : v2, 1));
+            k1 = __fadd_rn(k1, __shfl_xor_sync(0xffffffffu, b0 ? v1 : v3, 1));
+            k = __fadd_rn(b1 ? k1 : k0, __shfl_xor_sync(0xffffffffu, b1 ? k0 : k1, 2));
+        } else {
+            k = __fadd_rn(v0, __shfl_xor_sync(0xffffffffu, v0, 1));
+            k = __fadd_rn(k, __shfl_xor_sync(0xffffffffu, k, 2));
+        }
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) k = __fadd_rn(k, __shfl_xor_sync(0xffffffffu, k, o));
-        s[0] = __shfl_sync(0xffffffffu, k, 0);
-        s[1] = __shfl_sync(0xffffffffu, k, 2);
-        s[2] = __shfl_sync(0xffffffffu, k, 1);
-        s[3] = __shfl_sync(0xffffffffu, k, 3);
+        const int at = i + 1 < N ? 2 * (lane & 1) + (lane >> 1) : 0;
+        if (lane < 4 && i + at < N) part[(i + at) * step] = k;
     }
 }
 
-// Columns of segment s of a D-column row.
-__device__ __forceinline__ int seg_cols(int s, int D) { return min(SEG, D - s * SEG); }
-
-// One segment of R rows: lane `lane` holds chunk `lane` of each row (zeros
-// past the end of the row, `live` false there). part[r * stride + seg] =
-// (mean, M2) of the segment.
-template <int R>
-__device__ __forceinline__ void segment_stats(const float2 (&v)[R][4], bool live, bool center, int n, int lane,
-                                              float2* part, int stride) {
-    float mean[R], m2[R];
-    if (center) {
+// The row's total from its segments' totals, for every lane of a warp.
+__device__ __forceinline__ float join_total(const float* part, int nseg, int lane) {
+    float sum = 0.0f;
+    for (int s = 0; s < nseg; s += 32) {  // two groups of 16 at a time
+        float v = s + lane < nseg ? part[s + lane] : 0.0f;
 #pragma unroll
-        for (int r = 0; r < R; ++r) mean[r] = chunk_sum(v[r]);
-        warp_sums<R>(mean, lane);
-        const float inv = __frcp_rn(static_cast<float>(n));
-#pragma unroll
-        for (int r = 0; r < R; ++r) mean[r] = __fmul_rn(mean[r], inv);
-    } else {
-#pragma unroll
-        for (int r = 0; r < R; ++r) mean[r] = 0.0f;
+        for (int o = 1; o < 16; o <<= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, o));
+        const float w = __shfl_xor_sync(0xffffffffu, v, 16);
+        sum = __fadd_rn(sum, lane < 16 ? v : w);
+        sum = __fadd_rn(sum, lane < 16 ? w : v);
     }
+    return sum;
+}
+// As join_total for two rows at once.
+__device__ __forceinline__ float2 join_totals2(const float* part0, const float* part1, int nseg, int lane) {
+    const float* part = lane < 16 ? part0 : part1;
+    float sum = 0.0f;
+    for (int s = 0; s < nseg; s += 16) {
+        float v = s + (lane & 15) < nseg ? part[s + (lane & 15)] : 0.0f;
 #pragma unroll
-    for (int r = 0; r < R; ++r) m2[r] = live ? chunk_m2(v[r], mean[r]) : 0.0f;
-    warp_sums<R>(m2, lane);
-    if (lane < R) {
-        float a = mean[0], b = m2[0];
-#pragma unroll
-        for (int r = 1; r < R; ++r) {
-            a = lane == r ? mean[r] : a;
-            b = lane == r ? m2[r] : b;
-        }
-        part[lane * stride] = make_float2(a, b);
+        for (int o = 1; o < 16; o <<= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, o));
+        sum = __fadd_rn(sum, v);
     }
+    const float other = __shfl_xor_sync(0xffffffffu, sum, 16);
+    return lane < 16 ? make_float2(sum, other) : make_float2(other, sum);
 }
 
-// Mean and 1 / sqrt(M2 / D + eps) of one row from its segments (called by
-// all lanes of a warp; each group of eight lanes joins a row of its own,
-// lanes 8g .. 8g + 7 the segments of `part`, which may differ by group).
-__device__ __forceinline__ float2 join_segments(const float2* part, int nseg, int D, bool center, float eps,
-                                                int lane) {
-    const int p = lane & 7;
-    float mean = 0.0f;
-    if (center) {
-        for (int s = p; s < nseg; s += 8)
-            mean = __fmaf_rn(static_cast<float>(seg_cols(s, D)), part[s].x, mean);
-#pragma unroll
-        for (int o = 1; o < 8; o <<= 1) mean = __fadd_rn(mean, __shfl_xor_sync(0xffffffffu, mean, o));
-        mean = __fdiv_rn(mean, static_cast<float>(D));
-    }
-    float m2 = 0.0f;
-    for (int s = p; s < nseg; s += 8) {
-        const float2 e = part[s];
-        const float d = __fadd_rn(e.x, -mean);
-        m2 = __fadd_rn(m2, __fmaf_rn(__fmul_rn(d, d), static_cast<float>(seg_cols(s, D)), e.y));
-    }
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) m2 = __fadd_rn(m2, __shfl_xor_sync(0xffffffffu, m2, o));
-    return make_float2(mean, __frsqrt_rn(__fadd_rn(__fdiv_rn(m2, static_cast<float>(D)), eps)));
-}
-
-// Statistics of R rows (<= 4) for every lane: rows in groups of eight lanes.
-template <int R>
-__device__ __forceinline__ void join_rows(const float2* part, int stride, int nseg, int D, bool center, float eps,
-                                          int lane, float2 (&st)[R]) {
-    const int row = (lane >> 3) % R;
-    const float2 mine = join_segments(part + row * stride, nseg, D, center, eps, lane);
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-        st[r] = make_float2(__shfl_sync(0xffffffffu, mine.x, 8 * r), __shfl_sync(0xffffffffu, mine.y, 8 * r));
+// 1 / sqrt(M2 / D + eps), inv_d = 1 / D.
+__device__ __forceinline__ float inverse_deviation(float m2, float inv_d, float eps) {
+    return rsqrtf(__fmaf_rn(m2, inv_d, eps));
 }
 
 // (x - mean) * rstd on a pair.

@@ -1087,8 +1087,9 @@ __global__ void __launch_bounds__(QA_THREADS) norm_quantize_kernel(QuantParams p
     extern __shared__ __align__(128) uint8_t smem[];
     const int nb = p.Kbp >> 5, nchunk = p.K / norm::CHUNK, nseg = (p.K + norm::SEG - 1) / norm::SEG;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    float2* part = reinterpret_cast<float2*>(smem);
-    uint8_t* sbuf = smem + ((nseg * 8 + 15) & ~15);
+    float* part = reinterpret_cast<float*>(smem);  // [2][nseg]
+    uint8_t* sbuf = smem + ((2 * nseg * 4 + 15) & ~15);
+    const float inv_d = __frcp_rn(static_cast<float>(p.K));
     const bool center = s.kind == OSM_NORM_LAYER;
     {
         const int npb = p.Kbp - p.Kb, npad = npb + (p.kp - p.k);
@@ -1101,22 +1102,29 @@ __global__ void __launch_bounds__(QA_THREADS) norm_quantize_kernel(QuantParams p
     }
     for (int64_t t = blockIdx.x; t < p.M; t += gridDim.x) {
         const size_t base = static_cast<size_t>(t) * p.K;
-        for (int seg = warp; seg < nseg; seg += QA_THREADS / 32) {
-            const int c = seg * 32 + lane;
-            float2 v[1][4];
-            const uint4 z = make_uint4(0, 0, 0, 0);
-            if constexpr (F32) {
-                const uint4* at = reinterpret_cast<const uint4*>(static_cast<const float*>(X) + base) + 2 * c;
-                norm::unpack(c < nchunk ? at[0] : z, c < nchunk ? at[1] : z, v[0]);
-            } else {
-                const uint4* at = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(X) + base) + c;
-                norm::unpack(c < nchunk ? at[0] : z, v[0]);
+        // a total over the row of one value per chunk
+        auto total = [&](float* at, auto value) -> float {
+            for (int seg = warp; seg < nseg; seg += QA_THREADS / 32) {
+                const int c = seg * 32 + lane;
+                float2 v[4];
+                const uint4 z = make_uint4(0, 0, 0, 0);
+                if constexpr (F32) {
+                    const uint4* from = reinterpret_cast<const uint4*>(static_cast<const float*>(X) + base) + 2 * c;
+                    norm::unpack(c < nchunk ? from[0] : z, c < nchunk ? from[1] : z, v);
+                } else {
+                    const uint4* from = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(X) + base) + c;
+                    norm::unpack(c < nchunk ? *from : z, v);
+                }
+                const float one[1] = {c < nchunk ? value(v) : 0.0f};
+                norm::warp_totals<1>(one, lane, at + seg, 1);
             }
-            norm::segment_stats<1>(v, c < nchunk, center, norm::seg_cols(seg, p.K), lane, part + seg, 0);
-        }
-        __syncthreads();
-        float2 st[1];
-        norm::join_rows<1>(part, 0, nseg, p.K, center, s.eps, lane, st);
+            __syncthreads();
+            return norm::join_total(at, nseg, lane);
+        };
+        float mean = 0.0f;
+        if (center) mean = __fmul_rn(total(part, [](const float2 (&v)[4]) { return norm::chunk_sum(v); }), inv_d);
+        const float m2 = total(part + nseg, [&](const float2 (&v)[4]) { return norm::chunk_m2(v, mean); });
+        const float2 st[1] = {make_float2(mean, norm::inverse_deviation(m2, inv_d, s.eps))};
         const int64_t mrow = s.scale || s.shift ? t / s.mod_rows : 0;
         for (int c = tid; c < (p.K >> 1); c += QA_THREADS) {
             float2 x, a, b;
@@ -1324,7 +1332,7 @@ int launch_norm_quantize(const osm_plan* pl, const void* X, int x_dtype, int64_t
                        spec->mod_rows > 0 ? spec->mod_rows : 1, spec->mod_stride};
     const int mode = pl->fmt == OSM_FMT_NVFP4 ? QA_NV : (pl->hp_fp16 ? QA_MX_F16 : QA_MX);
     const int nseg = static_cast<int>(ceil_div(pl->K, norm::SEG));
-    const size_t smem = ((nseg * 8 + 15) & ~15) + qa_row_stride(static_cast<int>(pl->Kbp / 32), static_cast<int>(pl->kp));
+    const size_t smem = ((2 * nseg * 4 + 15) & ~15) + qa_row_stride(static_cast<int>(pl->Kbp / 32), static_cast<int>(pl->kp));
     auto pick = [&](auto f) {
         constexpr bool F = decltype(f)::value;
         return mode == QA_NV ? norm_quantize_kernel<QA_NV, F>

@@ -83,7 +83,7 @@ def test_the_binding_refuses_host_tensors_and_wrong_types():
     with pytest.raises(ValueError, match="float32 CUDA"):
         osm.Norm(scale=torch.zeros(64)).spec(4, 64)
     with pytest.raises(ValueError, match="CUDA"):
-        osm.Norm(weight=torch.zeros(64)).spec(4, 64)
+        osm.Norm(weight=torch.zeros(64)).spec(4, 64, 0)
     with pytest.raises(ValueError, match="pre"):
         osm.residual_norm(x, x, out=x, h=x)
     with pytest.raises(ValueError, match="dtype"):
