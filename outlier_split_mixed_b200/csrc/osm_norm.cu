@@ -322,9 +322,11 @@ template <bool F32, bool HAS_Y>
 int launch_width(const RowParams& p, cudaStream_t st) {
     // Tiles pay once a CTA has a row for each of its 16 warps (M from about
     // 2400 rows on) and runs long enough to lay out their coefficients once.
-    const bool tiles = p.M >= 148 * 16 && p.share >= 64 && p.D <= 8192;
+    // The coefficients of 14336 columns (both tables) fill shared memory.
+    const bool tiles = p.M >= 148 * 16 && p.share >= 64 && p.D <= 14336;
     if (!tiles) {
         if (p.D <= 8192) return launch_single<F32, HAS_Y, 2, 2>(p, st);
+        if (p.D <= 16384) return launch_single<F32, HAS_Y, 4, F32 ? 1 : 2>(p, st);
         return launch_single<F32, HAS_Y, 16, 1>(p, st);
     }
     if (p.D <= 512) return launch_tiles<F32, HAS_Y, 1, 2, 2>(p, st);
@@ -333,7 +335,9 @@ int launch_width(const RowParams& p, cudaStream_t st) {
     constexpr int W = F32 ? (HAS_Y ? 4 : 2) : (HAS_Y ? 2 : 1);
     if (p.D <= 5120) return launch_tiles<F32, HAS_Y, W, 20 / W, 1>(p, st);
     constexpr int V = F32 || HAS_Y ? 4 : 2;
-    return launch_tiles<F32, HAS_Y, V, 32 / V, 1>(p, st);
+    if (p.D <= 8192) return launch_tiles<F32, HAS_Y, V, 32 / V, 1>(p, st);
+    constexpr int U = F32 || HAS_Y ? 8 : 4;
+    return launch_tiles<F32, HAS_Y, U, 56 / U, 1>(p, st);
 }
 
 Spec to_spec(const osm_norm_spec* s) {

@@ -1148,6 +1148,240 @@ __global__ void __launch_bounds__(QA_THREADS) norm_quantize_kernel(QuantParams p
     }
 }
 
+// Encode half a staged block (16 positions) of both rows of a pair: the words
+// are read once and stay in registers; the two lanes of an MXFP4 block
+// exchange their maxima. Called by whole warps, lanes 2i and 2i + 1 on the
+// halves of one block; `on` is false past the last block.
+template <int MODE>
+__device__ __forceinline__ void encode_pair_half(const QuantParams& p, uint32_t sbuf, int t0, int rows, int hb, bool on) {
+    const int b = hb >> 1, half = hb & 1;
+    const uint32_t src = sbuf + b * IP_BLOCK + half * 64;
+    const uint4 v0 = ptx::ld_shared_v4(src), v1 = ptx::ld_shared_v4(src + 16), v2 = ptx::ld_shared_v4(src + 32),
+                v3 = ptx::ld_shared_v4(src + 48);
+    using mx::bf16x2_absmax;
+    uint32_t m = bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(v0.x, v0.y), bf16x2_absmax(v0.z, v0.w)),
+                                             bf16x2_absmax(bf16x2_absmax(v1.x, v1.y), bf16x2_absmax(v1.z, v1.w))),
+                               bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(v2.x, v2.y), bf16x2_absmax(v2.z, v2.w)),
+                                             bf16x2_absmax(bf16x2_absmax(v3.x, v3.y), bf16x2_absmax(v3.z, v3.w))));
+    if constexpr (MODE != QA_NV) m = bf16x2_absmax(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    const uint32_t m0 = m & 0x7FFFu, m1 = (m >> 16) & 0x7FFFu;
+    if (!on) return;
+    float f0, f1;  // element multipliers of the two rows
+    if constexpr (MODE == QA_NV) {
+        const uint32_t s = mx::nv_block_scales(m0, m1, p.nv_k, p.nv_p2g, &f0, &f1);
+        p.scales[sf_offset(t0, hb, p.katoms)] = static_cast<uint8_t>(s);
+        if (rows == 2) p.scales[sf_offset(t0 + 1, hb, p.katoms)] = static_cast<uint8_t>(s >> 8);
+    } else {
+        const bool real = b * 32 < p.Kb;
+        const int X0 = mx::bf16_block_exponent(m0, &f0), X1 = mx::bf16_block_exponent(m1, &f1);
+        // the block's scale bytes: row 0 by the first lane, row 1 by the second
+        if (half == 0) p.scales[sf_offset(t0, b, p.katoms)] = static_cast<uint8_t>(real ? X0 + 127 : 0);
+        else if (rows == 2) p.scales[sf_offset(t0 + 1, b, p.katoms)] = static_cast<uint8_t>(real ? X1 + 127 : 0);
+    }
+    const uint32_t w[16] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w, v2.x, v2.y, v2.z, v2.w, v3.x, v3.y, v3.z, v3.w};
+    const size_t cstride = static_cast<size_t>(p.Kbp >> 1);
+    uint8_t* codes = p.codes + static_cast<size_t>(t0) * cstride + hb * 8;
+    *reinterpret_cast<uint2*>(codes) = make_uint2(encode8_halves<false>(w, f0), encode8_halves<false>(w + 8, f0));
+    if (rows == 2)
+        *reinterpret_cast<uint2*>(codes + cstride) = make_uint2(encode8_halves<true>(w, f1), encode8_halves<true>(w + 8, f1));
+}
+
+// The form for K <= 5120: persistent CTAs of one warp per 256-column segment
+// take two rows at a time (the ring of raw rows, the bounded waits and the
+// paired staging are quantize_act_pair_kernel's). Per pair of rows:
+//   statistics  warp w holds segment w of both rows in registers (one 128-bit
+//               shared load per row and lane) for the mean and the deviations;
+//               the segments are joined by every warp for itself;
+//   routing     each thread takes four channel pairs of both rows: normalise,
+//               modulate (coefficients of the run in shared memory, one
+//               128-bit load per channel pair for both rows), round, smooth,
+//               round, store at the routed words;
+//   encoding    half a block of both rows per thread.
+// Rows are paired inside the runs of tokens that share a modulation row.
+constexpr int NQ_THREADS = 640;  // at most; 32 per segment
+constexpr int NQ_TR = 4;         // channel pairs per thread (128 per segment)
+constexpr int NQ_STAGES = 2;
+
+__host__ __device__ constexpr int nq_smem_bytes(int K, int nb, int kp, int nseg, bool f32) {
+    return NQ_STAGES * 2 * K * (f32 ? 4 : 2) + K * 8 + ((qa_ip_bytes(nb, kp) + 15) & ~15) + ((4 * nseg * 4 + 15) & ~15) +
+           8 * NQ_STAGES;
+}
+
+template <int MODE, bool F32>
+__global__ void __launch_bounds__(NQ_THREADS, F32 ? 1 : 2)
+    norm_quantize_pair_kernel(QuantParams p, norm::Spec s, const void* X, uint32_t share, uint32_t groups_per_run,
+                              uint32_t groups) {
+    constexpr bool HPF = MODE == QA_MX_F16;
+    constexpr int XB = F32 ? 4 : 2;
+    ptx::grid_dep_launch();  // the dual_gemm that follows may start its prologue
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int NT = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int nb = p.Kbp >> 5, nseg = NT >> 5, npairs = p.K >> 1, nchunk = p.K / norm::CHUNK;
+    const int row_bytes = p.K * XB;
+    uint8_t* raw = smem;
+    float4* table = reinterpret_cast<float4*>(smem + NQ_STAGES * 2 * row_bytes);  // [K / 2] a, a, b, b
+    uint8_t* sbuf = reinterpret_cast<uint8_t*>(table + npairs);
+    float* part = reinterpret_cast<float*>(sbuf + ((qa_ip_bytes(nb, p.kp) + 15) & ~15));  // [2 sums][2 rows][nseg]
+    uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(part) + ((4 * nseg * 4 + 15) & ~15));
+    __shared__ int never;  // a flag nothing sets
+    const bool center = s.kind == OSM_NORM_LAYER;
+    const float inv_d = __frcp_rn(static_cast<float>(p.K));
+
+    struct Group {
+        uint32_t row0, run;
+        int rows;
+    };
+    auto group_of = [&](uint32_t g) -> Group {
+        const uint32_t M = static_cast<uint32_t>(p.M);
+        const uint32_t run = share >= M ? 0u : g / groups_per_run;
+        const uint32_t row0 = run * share + (g - run * groups_per_run) * 2;
+        const uint32_t end = min(M, run * share + share);
+        return {row0, run, row0 >= end ? 0 : static_cast<int>(min(2u, end - row0))};
+    };
+    // group i of this CTA into its slot (groups behind the last run's end have no rows: nothing to wait for)
+    auto issue = [&](uint32_t i) {
+        const Group gr = group_of(blockIdx.x + i * gridDim.x);
+        const uint32_t bar = ptx::smem_u32(&full[i % NQ_STAGES]);
+        const uint32_t bytes = static_cast<uint32_t>(gr.rows) * row_bytes;
+        ptx::mbar_arrive_expect_tx(bar, bytes + p.extra_tx);
+        if (bytes)
+            ptx::bulk_load(ptx::smem_u32(raw + (i % NQ_STAGES) * 2 * row_bytes),
+                           static_cast<const uint8_t*>(X) + static_cast<size_t>(gr.row0) * row_bytes, bytes, bar);
+    };
+    const uint32_t mine = blockIdx.x < groups ? (groups - 1 - blockIdx.x) / gridDim.x + 1 : 0;
+    if (tid == 0) {
+        for (int i = 0; i < NQ_STAGES; ++i) ptx::mbar_init(ptx::smem_u32(&full[i]), 1);
+        never = 0;
+        ptx::fence_mbar_init();
+    }
+    // padding positions (bulk [Kb, Kbp), slots [k, kp)) of both rows: zeroed once
+    {
+        const int npb = p.Kbp - p.Kb, npad = npb + (p.kp - p.k);
+        for (int c = tid; c < npad; c += NT) {
+            const int pos = p.Kb + c;
+            const int off = c < npb ? (pos >> 5) * IP_BLOCK + (pos & 31) * 4 : nb * IP_BLOCK + (p.k + c - npb) * 4;
+            *reinterpret_cast<uint32_t*>(sbuf + off) = 0u;
+        }
+    }
+    __syncthreads();
+    uint32_t issued = 0;
+    if (tid == 0)
+        for (; issued < NQ_STAGES && issued < mine; ++issued) issue(issued);
+
+    const uint32_t raw_u32 = ptx::smem_u32(raw), sbuf_u32 = ptx::smem_u32(sbuf), table_u32 = ptx::smem_u32(table);
+    auto ip_off = [&](int off) -> int {  // as in quantize_act_pair_kernel
+        if (off < nb * QA_BLOCK_BYTES) {
+            const int b = off / QA_BLOCK_BYTES;
+            return b * IP_BLOCK + ((off - b * QA_BLOCK_BYTES) >> 1) * 4;
+        }
+        return nb * IP_BLOCK + ((off - nb * QA_BLOCK_BYTES) >> 1) * 4;
+    };
+    float2 tsv[NQ_TR];
+    uint32_t tad[NQ_TR];             // staged offsets of the pair's channels, 16 bits each (in words)
+    uint32_t tmask[HPF ? NQ_TR : 1]; // FP16 outlier branch: halves that are outlier slots
+#pragma unroll
+    for (int j = 0; j < NQ_TR; ++j) {
+        const int c = tid + j * NT;
+        tsv[j] = c < npairs ? __ldg(reinterpret_cast<const float2*>(p.inv_s) + c) : make_float2(0.f, 0.f);
+        const int2 dv = c < npairs ? __ldg(reinterpret_cast<const int2*>(p.route) + c) : make_int2(0, 0);
+        tad[j] = static_cast<uint32_t>(ip_off(dv.x) >> 2) | static_cast<uint32_t>(ip_off(dv.y) >> 2) << 16;
+        if constexpr (HPF) tmask[j] = slot_mask(dv, nb * QA_BLOCK_BYTES);
+    }
+    const int hv = p.kp >> 3, nhb = 2 * nb;
+    uint32_t held = 0xffffffffu;
+    for (uint32_t i = 0; i < mine; ++i) {
+        const Group gr = group_of(blockIdx.x + i * gridDim.x);
+        const uint32_t bar = ptx::smem_u32(&full[i % NQ_STAGES]);
+        const bool ok = ptx::mbar_wait_bounded(bar, (i / NQ_STAGES) & 1, p.wait_limit_ns, &never);
+        if (held != gr.run && gr.rows > 0) {  // uniform; the last group's readers are past its third barrier
+            held = gr.run;
+            const int64_t mrow = s.scale || s.shift ? gr.row0 / s.mod_rows : 0;
+            for (int c = tid; c < npairs; c += NT) {
+                float2 a, b;
+                norm::coefficients(s, mrow, 2 * c, a, b);
+                table[c] = make_float4(a.x, a.y, b.x, b.y);
+            }
+        }
+        // rows arrived, table complete, staged rows of the last group encoded
+        if (__syncthreads_or(!ok)) {
+            if (tid == 0) {
+                atomicOr(p.status, OSM_STATUS_TIMEOUT);
+                // let every copy already issued land in this CTA's shared memory
+                for (uint32_t j = i; j < issued; ++j)
+                    if (!ptx::mbar_wait_bounded(ptx::smem_u32(&full[j % NQ_STAGES]), (j / NQ_STAGES) & 1, 20000000ull,
+                                                &never))
+                        ptx::spin_ns(1000000);
+            }
+            __syncthreads();
+            return;
+        }
+        const uint32_t slot = raw_u32 + (i % NQ_STAGES) * 2 * row_bytes;
+        // statistics (row 1 of a one-row group repeats row 0)
+        const uint32_t next_row = gr.rows == 2 ? row_bytes : 0;
+        float2 st[2];
+        {
+            float2 v[2][4];
+            const bool live = tid < nchunk;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const uint32_t at = slot + r * next_row + tid * norm::CHUNK * XB;
+                const uint4 z = make_uint4(0, 0, 0, 0);
+                if constexpr (F32) norm::unpack(live ? ptx::ld_shared_v4(at) : z, live ? ptx::ld_shared_v4(at + 16) : z, v[r]);
+                else norm::unpack(live ? ptx::ld_shared_v4(at) : z, v[r]);
+            }
+            float2 mean = make_float2(0.0f, 0.0f);
+            if (center) {
+                const float sum[2] = {norm::chunk_sum(v[0]), norm::chunk_sum(v[1])};
+                norm::warp_totals<2>(sum, lane, part + warp, nseg);
+                __syncthreads();
+                mean = norm::join_totals2(part, part + nseg, nseg, lane);
+                mean = __fmul2_rn(mean, make_float2(inv_d, inv_d));
+            }
+            const float m2[2] = {live ? norm::chunk_m2(v[0], mean.x) : 0.0f, live ? norm::chunk_m2(v[1], mean.y) : 0.0f};
+            norm::warp_totals<2>(m2, lane, part + 2 * nseg + warp, nseg);
+            __syncthreads();
+            const float2 t = norm::join_totals2(part + 2 * nseg, part + 3 * nseg, nseg, lane);
+            st[0] = make_float2(mean.x, norm::inverse_deviation(t.x, inv_d, s.eps));
+            st[1] = make_float2(mean.y, norm::inverse_deviation(t.y, inv_d, s.eps));
+        }
+#pragma unroll
+        for (int j = 0; j < NQ_TR; ++j) {
+            const int c = tid + j * NT;
+            if (c < npairs) {
+                const uint4 q = ptx::ld_shared_v4(table_u32 + c * 16);
+                const float2 a = make_float2(__uint_as_float(q.x), __uint_as_float(q.y)),
+                             b = make_float2(__uint_as_float(q.z), __uint_as_float(q.w));
+                uint32_t h[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const uint32_t at = slot + r * next_row + c * 2 * XB;
+                    float2 x;
+                    if constexpr (F32) {
+                        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(x.x), "=f"(x.y) : "r"(at) : "memory");
+                    } else {
+                        const uint32_t w = ptx::ld_shared_u32(at);
+                        x = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+                    }
+                    h[r] = norm_smooth2<HPF>(x, st[r], a, b, tsv[j], HPF ? tmask[j] : 0u);
+                }
+                ptx::st_shared_u32(sbuf_u32 + (tad[j] & 0xFFFFu) * 4, __byte_perm(h[0], h[1], 0x5410));
+                ptx::st_shared_u32(sbuf_u32 + (tad[j] >> 16) * 4, __byte_perm(h[0], h[1], 0x7632));
+            }
+        }
+        __syncthreads();  // raw slot consumed, staged rows complete
+        if (tid == 0 && issued < mine) issue(issued++);
+        if (gr.rows > 0) {
+            const int t0 = static_cast<int>(gr.row0);
+            for (int base = warp * 32; base < nhb; base += NT) {
+                const int hb = base + lane;
+                encode_pair_half<MODE>(p, sbuf_u32, t0, gr.rows, min(hb, nhb - 2 + (hb & 1)), hb < nhb);
+            }
+            for (int c = NT - 1 - tid; c < hv; c += NT) copy_pair_slots<MODE>(p, sbuf_u32, nb, t0, gr.rows, c);
+            if (gr.row0 <= p.M - 1u && p.M - 1u < gr.row0 + gr.rows) zero_padding_scale_rows(p);
+        }
+    }
+}
+
 template <int S>
 size_t pair_smem_bytes(int K, int nb, int kp) {
     return static_cast<size_t>(S) * 2 * K * 2 + ((qa_ip_bytes(nb, kp) + 7) & ~7) + 8 * S;
@@ -1332,6 +1566,27 @@ int launch_norm_quantize(const osm_plan* pl, const void* X, int x_dtype, int64_t
                        spec->mod_rows > 0 ? spec->mod_rows : 1, spec->mod_stride};
     const int mode = pl->fmt == OSM_FMT_NVFP4 ? QA_NV : (pl->hp_fp16 ? QA_MX_F16 : QA_MX);
     const int nseg = static_cast<int>(ceil_div(pl->K, norm::SEG));
+    const int64_t run = spec->scale || spec->shift ? (M < spec->mod_rows ? M : spec->mod_rows) : M;
+    if (pl->K <= 5120 && run >= 32) {
+        const size_t smem = nq_smem_bytes(static_cast<int>(pl->K), static_cast<int>(pl->Kbp / 32), static_cast<int>(pl->kp),
+                                          nseg, f32);
+        auto pick = [&](auto f) {
+            constexpr bool F = decltype(f)::value;
+            return mode == QA_NV ? norm_quantize_pair_kernel<QA_NV, F>
+                                 : (mode == QA_MX_F16 ? norm_quantize_pair_kernel<QA_MX_F16, F>
+                                                      : norm_quantize_pair_kernel<QA_MX, F>);
+        };
+        auto kern = f32 ? pick(std::true_type{}) : pick(std::false_type{});
+        int per_sm = 0, sms = 0;
+        int rc = prepare_kernel(reinterpret_cast<const void*>(kern), 32 * nseg, smem, &per_sm, &sms);
+        if (rc) return rc;
+        if (per_sm < 1) return fail(OSM_ERR_UNSUPPORTED, "norm_quantize_act: no CTA fits (K = %lld)", (long long)pl->K);
+        const uint32_t per_run = static_cast<uint32_t>(ceil_div(run, 2));
+        const uint32_t groups = static_cast<uint32_t>(ceil_div(M, run)) * per_run;
+        const uint32_t grid = groups < static_cast<uint32_t>(sms * per_sm) ? groups : static_cast<uint32_t>(sms * per_sm);
+        kern<<<grid, 32 * nseg, smem, st>>>(p, s, X, static_cast<uint32_t>(run), per_run, groups);
+        return check_cuda(cudaGetLastError(), "norm_quantize_act launch");
+    }
     const size_t smem = ((2 * nseg * 4 + 15) & ~15) + qa_row_stride(static_cast<int>(pl->Kbp / 32), static_cast<int>(pl->kp));
     auto pick = [&](auto f) {
         constexpr bool F = decltype(f)::value;
