@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(ROWS_THREADS, MINB) rows_kernel(const __grid_c
         norm::warp_totals<NS>(v, lane, at + j, W);
         if constexpr (W == 1) __syncwarp();
         else asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(32 * W) : "memory");
-        return norm::join_total(at, nseg, lane);
+        return norm::join_total<W * NS>(at, nseg, lane);
     };
     auto coef = [&](int which, int c, float2 (&a)[4], float2 (&b)[4]) {
         const float4* at = table + (HAS_Y && which ? 4 : 0) * nchunk + c;
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(512, MINB) row_kernel(const __grid_constant__ 
         flip ^= 1;
         norm::warp_totals<NS>(v, lane, at + j, nw);
         __syncthreads();
-        return norm::join_total(at, nseg, lane);
+        return norm::join_total<16 * NS>(at, nseg, lane);
     };
     for (uint64_t row = blockIdx.x; row < p.M; row += gridDim.x) {
         const uint32_t r = static_cast<uint32_t>(row);

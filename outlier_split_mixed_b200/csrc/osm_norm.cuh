@@ -91,10 +91,15 @@ __device__ __forceinline__ void warp_totals(const float (&s)[N], int lane, float
     }
 }
 
-// The row's total from its segments' totals, for every lane of a warp.
+// The row's total from its segments' totals (at most MAX of them), for every
+// lane of a warp. Groups of 16 that are not there add zeros. (The trip counts
+// are constants: a loop over a run-time count costs three times the
+// instructions of its body here.)
+template <int MAX>
 __device__ __forceinline__ float join_total(const float* part, int nseg, int lane) {
     float sum = 0.0f;
-    for (int s = 0; s < nseg; s += 32) {  // two groups of 16 at a time
+#pragma unroll 1
+    for (int s = 0; s < (MAX + 31) / 32 * 32; s += 32) {  // two groups of 16 at a time
         float v = s + lane < nseg ? part[s + lane] : 0.0f;
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, o));
@@ -104,18 +109,19 @@ __device__ __forceinline__ float join_total(const float* part, int nseg, int lan
     }
     return sum;
 }
-// As join_total for two rows at once.
+// As join_total for two rows of at most 32 segments at once.
 __device__ __forceinline__ float2 join_totals2(const float* part0, const float* part1, int nseg, int lane) {
     const float* part = lane < 16 ? part0 : part1;
-    float sum = 0.0f;
-    for (int s = 0; s < nseg; s += 16) {
-        float v = s + (lane & 15) < nseg ? part[s + (lane & 15)] : 0.0f;
+    const int s = lane & 15;
+    float v = s < nseg ? part[s] : 0.0f, w = s + 16 < nseg ? part[s + 16] : 0.0f;
 #pragma unroll
-        for (int o = 1; o < 16; o <<= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, o));
-        sum = __fadd_rn(sum, v);
+    for (int o = 1; o < 16; o <<= 1) {
+        v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, o));
+        w = __fadd_rn(w, __shfl_xor_sync(0xffffffffu, w, o));
     }
-    const float other = __shfl_xor_sync(0xffffffffu, sum, 16);
-    return lane < 16 ? make_float2(sum, other) : make_float2(other, sum);
+    v = __fadd_rn(v, w);
+    const float other = __shfl_xor_sync(0xffffffffu, v, 16);
+    return lane < 16 ? make_float2(v, other) : make_float2(other, v);
 }
 
 // 1 / sqrt(M2 / D + eps), inv_d = 1 / D.

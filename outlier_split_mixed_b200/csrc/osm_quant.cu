@@ -571,6 +571,37 @@ __global__ void __launch_bounds__(QA_THREADS) quantize_act_kernel(QuantParams p)
 }
 
 
+// One 32-block of row t: its maxima, scale(s) and codes from its 32 staged
+// values (16 words).
+template <int MODE>
+__device__ __forceinline__ void encode_block(const QuantParams& p, int t, int b, uint4 q0, uint4 q1, uint4 q2, uint4 q3) {
+    const int katoms = p.katoms;
+    using mx::bf16x2_absmax;
+    const uint32_t m01 = bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(q0.x, q0.y), bf16x2_absmax(q0.z, q0.w)),
+                                       bf16x2_absmax(bf16x2_absmax(q1.x, q1.y), bf16x2_absmax(q1.z, q1.w)));
+    const uint32_t m23 = bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(q2.x, q2.y), bf16x2_absmax(q2.z, q2.w)),
+                                       bf16x2_absmax(bf16x2_absmax(q3.x, q3.y), bf16x2_absmax(q3.z, q3.w)));
+    uint8_t* codes = p.codes + static_cast<size_t>(t) * (p.Kbp >> 1) + b * 16;
+    if constexpr (MODE == QA_NV) {
+        float r_lo, r_hi;
+        const uint32_t s2 = mx::nv_block_scales(max(m01 & 0x7FFFu, (m01 >> 16) & 0x7FFFu),
+                                                max(m23 & 0x7FFFu, (m23 >> 16) & 0x7FFFu), p.nv_k, p.nv_p2g,
+                                                &r_lo, &r_hi);
+        *reinterpret_cast<uint4*>(codes) = make_uint4(encode8_words(q0, r_lo), encode8_words(q1, r_lo),
+                                                      encode8_words(q2, r_hi), encode8_words(q3, r_hi));
+        // 16-blocks 2b and 2b + 1: adjacent bytes of one atom row
+        *reinterpret_cast<uint16_t*>(p.scales + sf_offset(t, 2 * b, katoms)) = static_cast<uint16_t>(s2);
+    } else {
+        const uint32_t m = bf16x2_absmax(m01, m23);
+        const uint32_t amax = max(m & 0x7FFFu, (m >> 16) & 0x7FFFu);
+        float inv;
+        const int X = mx::bf16_block_exponent(amax, &inv);
+        *reinterpret_cast<uint4*>(codes) = make_uint4(encode8_words(q0, inv), encode8_words(q1, inv),
+                                                      encode8_words(q2, inv), encode8_words(q3, inv));
+        p.scales[sf_offset(t, b, katoms)] = static_cast<uint8_t>(b * 32 < p.Kb ? X + 127 : 0);
+    }
+}
+
 // Encode the staged rows [0, nrows) of a routed buffer: one thread per
 // (row, 32-block) -- four 128-bit shared loads, amax by packed u16 max, the
 // block scale(s), sixteen E2M1x2 conversions, one 16-byte code store and the
@@ -582,7 +613,6 @@ template <int MODE>
 __device__ __forceinline__ void encode_staged(const QuantParams& p, uint32_t sbuf, int stride, int row0,
                                               int nrows) {
     const int nb = p.Kbp >> 5;
-    const int katoms = p.katoms;
     const int tid = threadIdx.x;
     const float inv_nb = 1.0f / static_cast<float>(nb);
     for (int wi = tid; wi < nrows * nb; wi += blockDim.x) {
@@ -595,30 +625,7 @@ __device__ __forceinline__ void encode_staged(const QuantParams& p, uint32_t sbu
         const uint32_t src = sbuf + r * stride + b * QA_BLOCK_BYTES;
         const uint4 q0 = ptx::ld_shared_v4(src), q1 = ptx::ld_shared_v4(src + 16), q2 = ptx::ld_shared_v4(src + 32),
                     q3 = ptx::ld_shared_v4(src + 48);
-        using mx::bf16x2_absmax;
-        const uint32_t m01 = bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(q0.x, q0.y), bf16x2_absmax(q0.z, q0.w)),
-                                           bf16x2_absmax(bf16x2_absmax(q1.x, q1.y), bf16x2_absmax(q1.z, q1.w)));
-        const uint32_t m23 = bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(q2.x, q2.y), bf16x2_absmax(q2.z, q2.w)),
-                                           bf16x2_absmax(bf16x2_absmax(q3.x, q3.y), bf16x2_absmax(q3.z, q3.w)));
-        uint8_t* codes = p.codes + static_cast<size_t>(t) * (p.Kbp >> 1) + b * 16;
-        if constexpr (MODE == QA_NV) {
-            float r_lo, r_hi;
-            const uint32_t s2 = mx::nv_block_scales(max(m01 & 0x7FFFu, (m01 >> 16) & 0x7FFFu),
-                                                    max(m23 & 0x7FFFu, (m23 >> 16) & 0x7FFFu), p.nv_k, p.nv_p2g,
-                                                    &r_lo, &r_hi);
-            *reinterpret_cast<uint4*>(codes) = make_uint4(encode8_words(q0, r_lo), encode8_words(q1, r_lo),
-                                                          encode8_words(q2, r_hi), encode8_words(q3, r_hi));
-            // 16-blocks 2b and 2b + 1: adjacent bytes of one atom row
-            *reinterpret_cast<uint16_t*>(p.scales + sf_offset(t, 2 * b, katoms)) = static_cast<uint16_t>(s2);
-        } else {
-            const uint32_t m = bf16x2_absmax(m01, m23);
-            const uint32_t amax = max(m & 0x7FFFu, (m >> 16) & 0x7FFFu);
-            float inv;
-            const int X = mx::bf16_block_exponent(amax, &inv);
-            *reinterpret_cast<uint4*>(codes) = make_uint4(encode8_words(q0, inv), encode8_words(q1, inv),
-                                                          encode8_words(q2, inv), encode8_words(q3, inv));
-            p.scales[sf_offset(t, b, katoms)] = static_cast<uint8_t>(b * 32 < p.Kb ? X + 127 : 0);
-        }
+        encode_block<MODE>(p, t, b, q0, q1, q2, q3);
     }
     const int hv = p.kp >> 3;
     for (int i = tid; i < nrows * hv; i += blockDim.x) {
@@ -1119,7 +1126,7 @@ __global__ void __launch_bounds__(QA_THREADS) norm_quantize_kernel(QuantParams p
                 norm::warp_totals<1>(one, lane, at + seg, 1);
             }
             __syncthreads();
-            return norm::join_total(at, nseg, lane);
+            return norm::join_total<256>(at, nseg, lane);
         };
         float mean = 0.0f;
         if (center) mean = __fmul_rn(total(part, [](const float2 (&v)[4]) { return norm::chunk_sum(v); }), inv_d);
@@ -1148,237 +1155,225 @@ __global__ void __launch_bounds__(QA_THREADS) norm_quantize_kernel(QuantParams p
     }
 }
 
-// Encode half a staged block (16 positions) of both rows of a pair: the words
-// are read once and stay in registers; the two lanes of an MXFP4 block
-// exchange their maxima. Called by whole warps, lanes 2i and 2i + 1 on the
-// halves of one block; `on` is false past the last block.
-template <int MODE>
-__device__ __forceinline__ void encode_pair_half(const QuantParams& p, uint32_t sbuf, int t0, int rows, int hb, bool on) {
-    const int b = hb >> 1, half = hb & 1;
-    const uint32_t src = sbuf + b * IP_BLOCK + half * 64;
-    const uint4 v0 = ptx::ld_shared_v4(src), v1 = ptx::ld_shared_v4(src + 16), v2 = ptx::ld_shared_v4(src + 32),
-                v3 = ptx::ld_shared_v4(src + 48);
-    using mx::bf16x2_absmax;
-    uint32_t m = bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(v0.x, v0.y), bf16x2_absmax(v0.z, v0.w)),
-                                             bf16x2_absmax(bf16x2_absmax(v1.x, v1.y), bf16x2_absmax(v1.z, v1.w))),
-                               bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(v2.x, v2.y), bf16x2_absmax(v2.z, v2.w)),
-                                             bf16x2_absmax(bf16x2_absmax(v3.x, v3.y), bf16x2_absmax(v3.z, v3.w))));
-    if constexpr (MODE != QA_NV) m = bf16x2_absmax(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    const uint32_t m0 = m & 0x7FFFu, m1 = (m >> 16) & 0x7FFFu;
-    if (!on) return;
-    float f0, f1;  // element multipliers of the two rows
-    if constexpr (MODE == QA_NV) {
-        const uint32_t s = mx::nv_block_scales(m0, m1, p.nv_k, p.nv_p2g, &f0, &f1);
-        p.scales[sf_offset(t0, hb, p.katoms)] = static_cast<uint8_t>(s);
-        if (rows == 2) p.scales[sf_offset(t0 + 1, hb, p.katoms)] = static_cast<uint8_t>(s >> 8);
-    } else {
-        const bool real = b * 32 < p.Kb;
-        const int X0 = mx::bf16_block_exponent(m0, &f0), X1 = mx::bf16_block_exponent(m1, &f1);
-        // the block's scale bytes: row 0 by the first lane, row 1 by the second
-        if (half == 0) p.scales[sf_offset(t0, b, p.katoms)] = static_cast<uint8_t>(real ? X0 + 127 : 0);
-        else if (rows == 2) p.scales[sf_offset(t0 + 1, b, p.katoms)] = static_cast<uint8_t>(real ? X1 + 127 : 0);
+// The form for many rows of at most 5120 columns. Issue slots bound it (the
+// rows are read once), so a row pair stays with one team of two warps and the
+// team meets only four times per pair; the other teams of the CTA fill in:
+//   each lane holds chunks of 8 columns of both rows in registers (one 128-bit
+//   load each) for the statistics, as in osm_norm.cu;
+//   it normalises, modulates, rounds, smooths and rounds them -- coefficients
+//   and inv_s of the run in shared memory, read once for both rows -- and
+//   stores the 16-bit values at their routed places in the team's staged rows;
+//   then the team encodes the staged rows, a 32-block per lane at a time.
+// Staged rows are unpadded: the four 16-byte units of 32-block b stand in the
+// order u ^ ((b / 2) & 3), which makes the encoding's 128-bit reads by
+// consecutive lanes conflict-free; the lanes of a quarter warp store their
+// chunk's four words each starting from another one, for the same reason (the
+// order is laid out in the route table).
+// Two teams' worth of FP32 rows would not fit the registers: one row per team.
+constexpr int NQ_W = 2;  // warps per team
+
+template <int NS>
+struct NormQuantShape {
+    static constexpr int COLS = NQ_W * NS * norm::SEG;         // widest row
+    static constexpr int STRIDE = 2 * (COLS + 128 + 64);       // bytes of one staged row (Kbp + kp <= K + 192)
+    static constexpr int TEAMS = NS > 4 ? 7 : 8;
+    static constexpr int THREADS = 32 * NQ_W * TEAMS;
+    static constexpr int smem(int K, int R) {
+        return TEAMS * (R * STRIDE + 2 * R * NQ_W * NS * 4) + (K / norm::CHUNK) * 7 * 16;
     }
-    const uint32_t w[16] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w, v2.x, v2.y, v2.z, v2.w, v3.x, v3.y, v3.z, v3.w};
-    const size_t cstride = static_cast<size_t>(p.Kbp >> 1);
-    uint8_t* codes = p.codes + static_cast<size_t>(t0) * cstride + hb * 8;
-    *reinterpret_cast<uint2*>(codes) = make_uint2(encode8_halves<false>(w, f0), encode8_halves<false>(w + 8, f0));
-    if (rows == 2)
-        *reinterpret_cast<uint2*>(codes + cstride) = make_uint2(encode8_halves<true>(w, f1), encode8_halves<true>(w + 8, f1));
+};
+
+// Words 0..3 one place down (by1) and two (by2), around the end.
+__device__ __forceinline__ void rotate_words(uint32_t (&w)[4], bool by1, bool by2) {
+    const uint32_t x0 = by1 ? w[1] : w[0], x1 = by1 ? w[2] : w[1], x2 = by1 ? w[3] : w[2], x3 = by1 ? w[0] : w[3];
+    w[0] = by2 ? x2 : x0;
+    w[1] = by2 ? x3 : x1;
+    w[2] = by2 ? x0 : x2;
+    w[3] = by2 ? x1 : x3;
 }
 
-// The form for K <= 5120: persistent CTAs of one warp per 256-column segment
-// take two rows at a time (the ring of raw rows, the bounded waits and the
-// paired staging are quantize_act_pair_kernel's). Per pair of rows:
-//   statistics  warp w holds segment w of both rows in registers (one 128-bit
-//               shared load per row and lane) for the mean and the deviations;
-//               the segments are joined by every warp for itself;
-//   routing     each thread takes four channel pairs of both rows: normalise,
-//               modulate (coefficients of the run in shared memory, one
-//               128-bit load per channel pair for both rows), round, smooth,
-//               round, store at the routed words;
-//   encoding    half a block of both rows per thread.
-// Rows are paired inside the runs of tokens that share a modulation row.
-constexpr int NQ_THREADS = 640;  // at most; 32 per segment
-constexpr int NQ_TR = 4;         // channel pairs per thread (128 per segment)
-constexpr int NQ_STAGES = 2;
-
-__host__ __device__ constexpr int nq_smem_bytes(int K, int nb, int kp, int nseg, bool f32) {
-    return NQ_STAGES * 2 * K * (f32 ? 4 : 2) + K * 8 + ((qa_ip_bytes(nb, kp) + 15) & ~15) + ((4 * nseg * 4 + 15) & ~15) +
-           8 * NQ_STAGES;
-}
-
-template <int MODE, bool F32>
-__global__ void __launch_bounds__(NQ_THREADS, F32 ? 1 : 2)
-    norm_quantize_pair_kernel(QuantParams p, norm::Spec s, const void* X, uint32_t share, uint32_t groups_per_run,
-                              uint32_t groups) {
+template <int MODE, bool F32, int NS, int MINB>
+__global__ void __launch_bounds__(NormQuantShape<NS>::THREADS, MINB)
+    norm_quantize_rows_kernel(QuantParams p, norm::Spec s, const void* X, uint32_t share, uint32_t tile_rows,
+                              uint32_t tiles_per_run, uint32_t tiles) {
+    using Shape = NormQuantShape<NS>;
     constexpr bool HPF = MODE == QA_MX_F16;
-    constexpr int XB = F32 ? 4 : 2;
+    constexpr int R = F32 ? 1 : 2;
+    constexpr int XQ = F32 ? 2 : 1;
+    constexpr int W = NQ_W;
     ptx::grid_dep_launch();  // the dual_gemm that follows may start its prologue
     extern __shared__ __align__(128) uint8_t smem[];
-    const int NT = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int nb = p.Kbp >> 5, nseg = NT >> 5, npairs = p.K >> 1, nchunk = p.K / norm::CHUNK;
-    const int row_bytes = p.K * XB;
-    uint8_t* raw = smem;
-    float4* table = reinterpret_cast<float4*>(smem + NQ_STAGES * 2 * row_bytes);  // [K / 2] a, a, b, b
-    uint8_t* sbuf = reinterpret_cast<uint8_t*>(table + npairs);
-    float* part = reinterpret_cast<float*>(sbuf + ((qa_ip_bytes(nb, p.kp) + 15) & ~15));  // [2 sums][2 rows][nseg]
-    uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(part) + ((4 * nseg * 4 + 15) & ~15));
-    __shared__ int never;  // a flag nothing sets
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, team = warp / W, j = warp % W, tt = tid % (32 * W);
+    const int nb = p.Kbp >> 5, nchunk = p.K / norm::CHUNK, nseg = (p.K + norm::SEG - 1) / norm::SEG, hv = p.kp >> 3;
     const bool center = s.kind == OSM_NORM_LAYER;
     const float inv_d = __frcp_rn(static_cast<float>(p.K));
+    // [TEAMS][R] staged rows, [TEAMS][2][R][W * NS] segment totals, the tables
+    const uint32_t stage = ptx::smem_u32(smem) + team * R * Shape::STRIDE;
+    float* part = reinterpret_cast<float*>(smem + Shape::TEAMS * R * Shape::STRIDE) + team * 2 * R * W * NS;
+    uint4* table = reinterpret_cast<uint4*>(smem + Shape::TEAMS * (R * Shape::STRIDE + 2 * R * W * NS * 4));
+    // words of chunk c: a, a, b, b (table[i * nchunk + c], i = 0..3), inv_s (4, 5), routes (6)
 
-    struct Group {
-        uint32_t row0, run;
-        int rows;
+    // staged byte of channel position `off` (an offset of the plan's route table)
+    auto staged = [&](int off) -> uint32_t {
+        if (off >= nb * QA_BLOCK_BYTES) return p.Kbp * 2 + (off - nb * QA_BLOCK_BYTES);
+        const int b = off / QA_BLOCK_BYTES, e = off - b * QA_BLOCK_BYTES;
+        return b * 64 + (((e >> 4) ^ (b >> 1)) & 3) * 16 + (e & 15);
     };
-    auto group_of = [&](uint32_t g) -> Group {
-        const uint32_t M = static_cast<uint32_t>(p.M);
-        const uint32_t run = share >= M ? 0u : g / groups_per_run;
-        const uint32_t row0 = run * share + (g - run * groups_per_run) * 2;
-        const uint32_t end = min(M, run * share + share);
-        return {row0, run, row0 >= end ? 0 : static_cast<int>(min(2u, end - row0))};
-    };
-    // group i of this CTA into its slot (groups behind the last run's end have no rows: nothing to wait for)
-    auto issue = [&](uint32_t i) {
-        const Group gr = group_of(blockIdx.x + i * gridDim.x);
-        const uint32_t bar = ptx::smem_u32(&full[i % NQ_STAGES]);
-        const uint32_t bytes = static_cast<uint32_t>(gr.rows) * row_bytes;
-        ptx::mbar_arrive_expect_tx(bar, bytes + p.extra_tx);
-        if (bytes)
-            ptx::bulk_load(ptx::smem_u32(raw + (i % NQ_STAGES) * 2 * row_bytes),
-                           static_cast<const uint8_t*>(X) + static_cast<size_t>(gr.row0) * row_bytes, bytes, bar);
-    };
-    const uint32_t mine = blockIdx.x < groups ? (groups - 1 - blockIdx.x) / gridDim.x + 1 : 0;
-    if (tid == 0) {
-        for (int i = 0; i < NQ_STAGES; ++i) ptx::mbar_init(ptx::smem_u32(&full[i]), 1);
-        never = 0;
-        ptx::fence_mbar_init();
+    for (int c = tid; c < nchunk; c += Shape::THREADS) {
+        const int2* rt = reinterpret_cast<const int2*>(p.route) + 4 * c;
+        uint32_t word[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // the word that a lane stores i-th
+            const int2 dv = __ldg(rt + ((i + ((c & 31) >> 3)) & 3));
+            word[i] = staged(dv.x) | staged(dv.y) << 16;
+        }
+        table[6 * nchunk + c] = make_uint4(word[0], word[1], word[2], word[3]);
+        table[4 * nchunk + c] = __ldg(reinterpret_cast<const uint4*>(p.inv_s) + 2 * c);
+        table[5 * nchunk + c] = __ldg(reinterpret_cast<const uint4*>(p.inv_s) + 2 * c + 1);
     }
-    // padding positions (bulk [Kb, Kbp), slots [k, kp)) of both rows: zeroed once
+    // padding positions (bulk [Kb, Kbp), slots [k, kp)) of the staged rows are zeroed once
     {
         const int npb = p.Kbp - p.Kb, npad = npb + (p.kp - p.k);
-        for (int c = tid; c < npad; c += NT) {
+        for (int i = tt; i < R * npad; i += 32 * W) {
+            const int r = i / npad, c = i - r * npad;
             const int pos = p.Kb + c;
-            const int off = c < npb ? (pos >> 5) * IP_BLOCK + (pos & 31) * 4 : nb * IP_BLOCK + (p.k + c - npb) * 4;
-            *reinterpret_cast<uint32_t*>(sbuf + off) = 0u;
+            const uint32_t at = c < npb ? staged((pos >> 5) * QA_BLOCK_BYTES + (pos & 31) * 2)
+                                        : static_cast<uint32_t>(p.Kbp * 2 + (p.k + c - npb) * 2);
+            ptx::st_shared_u16(stage + r * Shape::STRIDE + at, 0);
         }
     }
-    __syncthreads();
-    uint32_t issued = 0;
-    if (tid == 0)
-        for (; issued < NQ_STAGES && issued < mine; ++issued) issue(issued);
+    auto team_sync = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(32 * W) : "memory"); };
 
-    const uint32_t raw_u32 = ptx::smem_u32(raw), sbuf_u32 = ptx::smem_u32(sbuf), table_u32 = ptx::smem_u32(table);
-    auto ip_off = [&](int off) -> int {  // as in quantize_act_pair_kernel
-        if (off < nb * QA_BLOCK_BYTES) {
-            const int b = off / QA_BLOCK_BYTES;
-            return b * IP_BLOCK + ((off - b * QA_BLOCK_BYTES) >> 1) * 4;
-        }
-        return nb * IP_BLOCK + ((off - nb * QA_BLOCK_BYTES) >> 1) * 4;
-    };
-    float2 tsv[NQ_TR];
-    uint32_t tad[NQ_TR];             // staged offsets of the pair's channels, 16 bits each (in words)
-    uint32_t tmask[HPF ? NQ_TR : 1]; // FP16 outlier branch: halves that are outlier slots
-#pragma unroll
-    for (int j = 0; j < NQ_TR; ++j) {
-        const int c = tid + j * NT;
-        tsv[j] = c < npairs ? __ldg(reinterpret_cast<const float2*>(p.inv_s) + c) : make_float2(0.f, 0.f);
-        const int2 dv = c < npairs ? __ldg(reinterpret_cast<const int2*>(p.route) + c) : make_int2(0, 0);
-        tad[j] = static_cast<uint32_t>(ip_off(dv.x) >> 2) | static_cast<uint32_t>(ip_off(dv.y) >> 2) << 16;
-        if constexpr (HPF) tmask[j] = slot_mask(dv, nb * QA_BLOCK_BYTES);
-    }
-    const int hv = p.kp >> 3, nhb = 2 * nb;
     uint32_t held = 0xffffffffu;
-    for (uint32_t i = 0; i < mine; ++i) {
-        const Group gr = group_of(blockIdx.x + i * gridDim.x);
-        const uint32_t bar = ptx::smem_u32(&full[i % NQ_STAGES]);
-        const bool ok = ptx::mbar_wait_bounded(bar, (i / NQ_STAGES) & 1, p.wait_limit_ns, &never);
-        if (held != gr.run && gr.rows > 0) {  // uniform; the last group's readers are past its third barrier
-            held = gr.run;
-            const int64_t mrow = s.scale || s.shift ? gr.row0 / s.mod_rows : 0;
-            for (int c = tid; c < npairs; c += NT) {
-                float2 a, b;
-                norm::coefficients(s, mrow, 2 * c, a, b);
-                table[c] = make_float4(a.x, a.y, b.x, b.y);
-            }
-        }
-        // rows arrived, table complete, staged rows of the last group encoded
-        if (__syncthreads_or(!ok)) {
-            if (tid == 0) {
-                atomicOr(p.status, OSM_STATUS_TIMEOUT);
-                // let every copy already issued land in this CTA's shared memory
-                for (uint32_t j = i; j < issued; ++j)
-                    if (!ptx::mbar_wait_bounded(ptx::smem_u32(&full[j % NQ_STAGES]), (j / NQ_STAGES) & 1, 20000000ull,
-                                                &never))
-                        ptx::spin_ns(1000000);
+    for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        const uint32_t run = tile / tiles_per_run, first = run * share;
+        const uint32_t row0 = first + (tile - run * tiles_per_run) * tile_rows;
+        const uint32_t end = min(min(row0 + tile_rows, first + share), static_cast<uint32_t>(p.M));
+        if (held != run) {
+            if (held != 0xffffffffu) __syncthreads();  // the rows of the last run are done
+            held = run;
+            const int64_t mrow = s.scale || s.shift ? first / s.mod_rows : 0;
+            for (int i = tid; i < 2 * nchunk; i += Shape::THREADS) {
+                const int half = i >= nchunk, c = i - half * nchunk, col = c * norm::CHUNK + 4 * half;
+                float2 a0, a1, b0, b1;
+                norm::coefficients(s, mrow, col, a0, b0);
+                norm::coefficients(s, mrow, col + 2, a1, b1);
+                reinterpret_cast<float4*>(table)[half * nchunk + c] = make_float4(a0.x, a0.y, a1.x, a1.y);
+                reinterpret_cast<float4*>(table)[(2 + half) * nchunk + c] = make_float4(b0.x, b0.y, b1.x, b1.y);
             }
             __syncthreads();
-            return;
         }
-        const uint32_t slot = raw_u32 + (i % NQ_STAGES) * 2 * row_bytes;
-        // statistics (row 1 of a one-row group repeats row 0)
-        const uint32_t next_row = gr.rows == 2 ? row_bytes : 0;
-        float2 st[2];
-        {
-            float2 v[2][4];
-            const bool live = tid < nchunk;
+        for (uint32_t row = row0 + R * team; row < end; row += R * Shape::TEAMS) {
+            const int rows = R == 1 ? 1 : static_cast<int>(min(2u, end - row));
+            uint4 xq[R][NS][XQ];
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const uint32_t at = slot + r * next_row + tid * norm::CHUNK * XB;
-                const uint4 z = make_uint4(0, 0, 0, 0);
-                if constexpr (F32) norm::unpack(live ? ptx::ld_shared_v4(at) : z, live ? ptx::ld_shared_v4(at + 16) : z, v[r]);
-                else norm::unpack(live ? ptx::ld_shared_v4(at) : z, v[r]);
+            for (int t = 0; t < NS; ++t) {
+                const int c = (j + t * W) * 32 + lane;
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int q = 0; q < XQ; ++q)
+                        xq[r][t][q] = c < nchunk && r < rows
+                                          ? ldg_nc_v4(static_cast<const uint4*>(X) +
+                                                      (static_cast<size_t>(row + r) * nchunk + c) * XQ + q)
+                                          : make_uint4(0, 0, 0, 0);
             }
+            auto x_of = [&](int r, int t, float2 (&v)[4]) {
+                if constexpr (F32) norm::unpack(xq[r][t][0], xq[r][t][1], v);
+                else norm::unpack(xq[r][t][0], v);
+            };
+            // totals over each row of one value per chunk
+            float value[R][NS];
+            auto totals = [&](float* at) -> float2 {
+#pragma unroll
+                for (int r = 0; r < R; ++r) norm::warp_totals<NS>(value[r], lane, at + r * W * NS + j, W);
+                team_sync();
+                if (R == 2) return norm::join_totals2(at, at + W * NS, nseg, lane);
+                return make_float2(norm::join_total<W * NS>(at, nseg, lane), 0.0f);
+            };
             float2 mean = make_float2(0.0f, 0.0f);
             if (center) {
-                const float sum[2] = {norm::chunk_sum(v[0]), norm::chunk_sum(v[1])};
-                norm::warp_totals<2>(sum, lane, part + warp, nseg);
-                __syncthreads();
-                mean = norm::join_totals2(part, part + nseg, nseg, lane);
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int t = 0; t < NS; ++t) {
+                        float2 v[4];
+                        x_of(r, t, v);
+                        value[r][t] = norm::chunk_sum(v);
+                    }
+                mean = totals(part);
                 mean = __fmul2_rn(mean, make_float2(inv_d, inv_d));
             }
-            const float m2[2] = {live ? norm::chunk_m2(v[0], mean.x) : 0.0f, live ? norm::chunk_m2(v[1], mean.y) : 0.0f};
-            norm::warp_totals<2>(m2, lane, part + 2 * nseg + warp, nseg);
-            __syncthreads();
-            const float2 t = norm::join_totals2(part + 2 * nseg, part + 3 * nseg, nseg, lane);
-            st[0] = make_float2(mean.x, norm::inverse_deviation(t.x, inv_d, s.eps));
-            st[1] = make_float2(mean.y, norm::inverse_deviation(t.y, inv_d, s.eps));
-        }
 #pragma unroll
-        for (int j = 0; j < NQ_TR; ++j) {
-            const int c = tid + j * NT;
-            if (c < npairs) {
-                const uint4 q = ptx::ld_shared_v4(table_u32 + c * 16);
-                const float2 a = make_float2(__uint_as_float(q.x), __uint_as_float(q.y)),
-                             b = make_float2(__uint_as_float(q.z), __uint_as_float(q.w));
-                uint32_t h[2];
+            for (int r = 0; r < R; ++r)
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const uint32_t at = slot + r * next_row + c * 2 * XB;
-                    float2 x;
-                    if constexpr (F32) {
-                        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(x.x), "=f"(x.y) : "r"(at) : "memory");
-                    } else {
-                        const uint32_t w = ptx::ld_shared_u32(at);
-                        x = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-                    }
-                    h[r] = norm_smooth2<HPF>(x, st[r], a, b, tsv[j], HPF ? tmask[j] : 0u);
+                for (int t = 0; t < NS; ++t) {
+                    float2 v[4];
+                    x_of(r, t, v);
+                    value[r][t] = (j + t * W) * 32 + lane < nchunk ? norm::chunk_m2(v, r ? mean.y : mean.x) : 0.0f;
                 }
-                ptx::st_shared_u32(sbuf_u32 + (tad[j] & 0xFFFFu) * 4, __byte_perm(h[0], h[1], 0x5410));
-                ptx::st_shared_u32(sbuf_u32 + (tad[j] >> 16) * 4, __byte_perm(h[0], h[1], 0x7632));
+            const float2 m2 = totals(part + R * W * NS);
+            const float2 st[2] = {make_float2(mean.x, norm::inverse_deviation(m2.x, inv_d, s.eps)),
+                                  make_float2(mean.y, norm::inverse_deviation(m2.y, inv_d, s.eps))};
+            // (the barrier of the totals also comes after the encoding of the team's last rows)
+#pragma unroll
+            for (int t = 0; t < NS; ++t) {
+                const int c = (j + t * W) * 32 + lane;
+                if (c >= nchunk) continue;
+                const uint4* at = table + c;
+                const uint4 a0 = at[0], a1 = at[nchunk], b0 = at[2 * nchunk], b1 = at[3 * nchunk], s0 = at[4 * nchunk],
+                            s1 = at[5 * nchunk], rt = at[6 * nchunk];
+                auto pair = [](uint32_t x, uint32_t y) { return make_float2(__uint_as_float(x), __uint_as_float(y)); };
+                const float2 ca[4] = {pair(a0.x, a0.y), pair(a0.z, a0.w), pair(a1.x, a1.y), pair(a1.z, a1.w)};
+                const float2 cb[4] = {pair(b0.x, b0.y), pair(b0.z, b0.w), pair(b1.x, b1.y), pair(b1.z, b1.w)};
+                const float2 cs[4] = {pair(s0.x, s0.y), pair(s0.z, s0.w), pair(s1.x, s1.y), pair(s1.z, s1.w)};
+                const uint32_t to[4] = {rt.x, rt.y, rt.z, rt.w};
+                const bool by1 = lane & 8, by2 = lane & 16;
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    float2 v[4];
+                    x_of(r, t, v);
+                    uint32_t w[4], u[4];  // BF16, and binary16 for the slots of an FP16 outlier branch
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        w[i] = norm_smooth2<false>(v[i], st[r], ca[i], cb[i], cs[i], 0u);
+                        if constexpr (HPF) u[i] = norm_smooth2<true>(v[i], st[r], ca[i], cb[i], cs[i], 0xFFFFFFFFu);
+                    }
+                    rotate_words(w, by1, by2);  // word i -> place i - lane / 8
+                    if constexpr (HPF) {
+                        rotate_words(u, by1, by2);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t mask = ((to[i] & 0xFFFFu) >= p.Kbp * 2u ? 0x0000FFFFu : 0u) |
+                                                  ((to[i] >> 16) >= p.Kbp * 2u ? 0xFFFF0000u : 0u);
+                            w[i] = (w[i] & ~mask) | (u[i] & mask);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        ptx::st_shared_u16(stage + (to[i] & 0xFFFFu) + r * Shape::STRIDE, w[i]);
+                        ptx::st_shared_u16(stage + (to[i] >> 16) + r * Shape::STRIDE, w[i] >> 16);
+                    }
+                }
+            }
+            team_sync();  // staged rows complete
+#pragma unroll 1
+            for (int i = tt; i < rows * nb; i += 32 * W) {
+                const int r = i >= nb, b = i - r * nb, row_r = static_cast<int>(row) + r;
+                const uint32_t src = stage + r * Shape::STRIDE + b * 64;
+                const int x = (b >> 1) & 3;
+                encode_block<MODE>(p, row_r, b, ptx::ld_shared_v4(src + x * 16), ptx::ld_shared_v4(src + (1 ^ x) * 16),
+                                   ptx::ld_shared_v4(src + (2 ^ x) * 16), ptx::ld_shared_v4(src + (3 ^ x) * 16));
+            }
+#pragma unroll 1
+            for (int i = 32 * W - 1 - tt; i < rows * hv; i += 32 * W) {
+                const int r = i >= hv, c = i - r * hv;
+                uint4 v = ptx::ld_shared_v4(stage + r * Shape::STRIDE + p.Kbp * 2 + c * 16);
+                if constexpr (MODE == QA_NV) v = mx::scale_bf16x8(v, p.hp_scale);
+                *reinterpret_cast<uint4*>(p.hp + static_cast<size_t>(row + r) * p.kp + c * 8) = v;
             }
         }
-        __syncthreads();  // raw slot consumed, staged rows complete
-        if (tid == 0 && issued < mine) issue(issued++);
-        if (gr.rows > 0) {
-            const int t0 = static_cast<int>(gr.row0);
-            for (int base = warp * 32; base < nhb; base += NT) {
-                const int hb = base + lane;
-                encode_pair_half<MODE>(p, sbuf_u32, t0, gr.rows, min(hb, nhb - 2 + (hb & 1)), hb < nhb);
-            }
-            for (int c = NT - 1 - tid; c < hv; c += NT) copy_pair_slots<MODE>(p, sbuf_u32, nb, t0, gr.rows, c);
-            if (gr.row0 <= p.M - 1u && p.M - 1u < gr.row0 + gr.rows) zero_padding_scale_rows(p);
-        }
+        if (row0 < static_cast<uint32_t>(p.M) && end == static_cast<uint32_t>(p.M)) zero_padding_scale_rows(p);
     }
 }
 
@@ -1558,6 +1553,32 @@ static QuantParams quant_params(const osm_plan* pl, const uint16_t* X, int64_t M
                   pow2f(-pl->g_act)};
 }
 
+template <int NS, int MINB>
+static int launch_norm_quantize_rows(const QuantParams& p, int mode, const norm::Spec& s, const void* X, bool f32, int64_t M,
+                                     int64_t run, cudaStream_t st) {
+    auto pick = [&](auto f) {
+        constexpr bool F = decltype(f)::value;
+        return mode == QA_NV ? norm_quantize_rows_kernel<QA_NV, F, NS, MINB>
+                             : (mode == QA_MX_F16 ? norm_quantize_rows_kernel<QA_MX_F16, F, NS, MINB>
+                                                  : norm_quantize_rows_kernel<QA_MX, F, NS, MINB>);
+    };
+    auto kern = f32 ? pick(std::true_type{}) : pick(std::false_type{});
+    const size_t smem = NormQuantShape<NS>::smem(p.K, f32 ? 1 : 2);
+    int per_sm = 0, sms = 0;
+    int rc = prepare_kernel(reinterpret_cast<const void*>(kern), NormQuantShape<NS>::THREADS, smem, &per_sm, &sms);
+    if (rc) return rc;
+    if (per_sm < 1) return fail(OSM_ERR_UNSUPPORTED, "norm_quantize_act: no CTA fits (K = %d)", p.K);
+    // one tile per CTA: each run is cut into its part of them
+    const int64_t ctas = static_cast<int64_t>(sms) * per_sm;
+    const int64_t cuts = ctas * run / M > 1 ? ctas * run / M : 1;
+    const int64_t tile_rows = ceil_div(run, cuts), per_run = ceil_div(run, tile_rows);
+    const int64_t tiles = ceil_div(M, run) * per_run;
+    kern<<<static_cast<unsigned>(tiles < ctas ? tiles : ctas), NormQuantShape<NS>::THREADS, smem, st>>>(
+        p, s, X, static_cast<uint32_t>(run), static_cast<uint32_t>(tile_rows), static_cast<uint32_t>(per_run),
+        static_cast<uint32_t>(tiles));
+    return check_cuda(cudaGetLastError(), "norm_quantize_act launch");
+}
+
 int launch_norm_quantize(const osm_plan* pl, const void* X, int x_dtype, int64_t M, const osm_norm_spec* spec,
                          uint8_t* codes, uint8_t* scales, uint16_t* hp, cudaStream_t st) {
     const bool f32 = x_dtype == OSM_DT_F32;
@@ -1567,25 +1588,11 @@ int launch_norm_quantize(const osm_plan* pl, const void* X, int x_dtype, int64_t
     const int mode = pl->fmt == OSM_FMT_NVFP4 ? QA_NV : (pl->hp_fp16 ? QA_MX_F16 : QA_MX);
     const int nseg = static_cast<int>(ceil_div(pl->K, norm::SEG));
     const int64_t run = spec->scale || spec->shift ? (M < spec->mod_rows ? M : spec->mod_rows) : M;
-    if (pl->K <= 5120 && run >= 32) {
-        const size_t smem = nq_smem_bytes(static_cast<int>(pl->K), static_cast<int>(pl->Kbp / 32), static_cast<int>(pl->kp),
-                                          nseg, f32);
-        auto pick = [&](auto f) {
-            constexpr bool F = decltype(f)::value;
-            return mode == QA_NV ? norm_quantize_pair_kernel<QA_NV, F>
-                                 : (mode == QA_MX_F16 ? norm_quantize_pair_kernel<QA_MX_F16, F>
-                                                      : norm_quantize_pair_kernel<QA_MX, F>);
-        };
-        auto kern = f32 ? pick(std::true_type{}) : pick(std::false_type{});
-        int per_sm = 0, sms = 0;
-        int rc = prepare_kernel(reinterpret_cast<const void*>(kern), 32 * nseg, smem, &per_sm, &sms);
-        if (rc) return rc;
-        if (per_sm < 1) return fail(OSM_ERR_UNSUPPORTED, "norm_quantize_act: no CTA fits (K = %lld)", (long long)pl->K);
-        const uint32_t per_run = static_cast<uint32_t>(ceil_div(run, 2));
-        const uint32_t groups = static_cast<uint32_t>(ceil_div(M, run)) * per_run;
-        const uint32_t grid = groups < static_cast<uint32_t>(sms * per_sm) ? groups : static_cast<uint32_t>(sms * per_sm);
-        kern<<<grid, 32 * nseg, smem, st>>>(p, s, X, static_cast<uint32_t>(run), per_run, groups);
-        return check_cuda(cudaGetLastError(), "norm_quantize_act launch");
+    // Many rows: teams of warps (see norm_quantize_rows_kernel). Below about
+    // eight rows per SM its tables cost more than they save.
+    if (pl->K <= 5120 && run >= 64 && M >= 148 * 8) {
+        if (pl->K <= 1024) return launch_norm_quantize_rows<2, 2>(p, mode, s, X, f32, M, run, st);
+        return launch_norm_quantize_rows<10, 1>(p, mode, s, X, f32, M, run, st);
     }
     const size_t smem = ((2 * nseg * 4 + 15) & ~15) + qa_row_stride(static_cast<int>(pl->Kbp / 32), static_cast<int>(pl->kp));
     auto pick = [&](auto f) {
