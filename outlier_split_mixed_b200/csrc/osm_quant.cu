@@ -571,37 +571,6 @@ __global__ void __launch_bounds__(QA_THREADS) quantize_act_kernel(QuantParams p)
 }
 
 
-// One 32-block of row t: its maxima, scale(s) and codes from its 32 staged
-// values (16 words).
-template <int MODE>
-__device__ __forceinline__ void encode_block(const QuantParams& p, int t, int b, uint4 q0, uint4 q1, uint4 q2, uint4 q3) {
-    const int katoms = p.katoms;
-    using mx::bf16x2_absmax;
-    const uint32_t m01 = bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(q0.x, q0.y), bf16x2_absmax(q0.z, q0.w)),
-                                       bf16x2_absmax(bf16x2_absmax(q1.x, q1.y), bf16x2_absmax(q1.z, q1.w)));
-    const uint32_t m23 = bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(q2.x, q2.y), bf16x2_absmax(q2.z, q2.w)),
-                                       bf16x2_absmax(bf16x2_absmax(q3.x, q3.y), bf16x2_absmax(q3.z, q3.w)));
-    uint8_t* codes = p.codes + static_cast<size_t>(t) * (p.Kbp >> 1) + b * 16;
-    if constexpr (MODE == QA_NV) {
-        float r_lo, r_hi;
-        const uint32_t s2 = mx::nv_block_scales(max(m01 & 0x7FFFu, (m01 >> 16) & 0x7FFFu),
-                                                max(m23 & 0x7FFFu, (m23 >> 16) & 0x7FFFu), p.nv_k, p.nv_p2g,
-                                                &r_lo, &r_hi);
-        *reinterpret_cast<uint4*>(codes) = make_uint4(encode8_words(q0, r_lo), encode8_words(q1, r_lo),
-                                                      encode8_words(q2, r_hi), encode8_words(q3, r_hi));
-        // 16-blocks 2b and 2b + 1: adjacent bytes of one atom row
-        *reinterpret_cast<uint16_t*>(p.scales + sf_offset(t, 2 * b, katoms)) = static_cast<uint16_t>(s2);
-    } else {
-        const uint32_t m = bf16x2_absmax(m01, m23);
-        const uint32_t amax = max(m & 0x7FFFu, (m >> 16) & 0x7FFFu);
-        float inv;
-        const int X = mx::bf16_block_exponent(amax, &inv);
-        *reinterpret_cast<uint4*>(codes) = make_uint4(encode8_words(q0, inv), encode8_words(q1, inv),
-                                                      encode8_words(q2, inv), encode8_words(q3, inv));
-        p.scales[sf_offset(t, b, katoms)] = static_cast<uint8_t>(b * 32 < p.Kb ? X + 127 : 0);
-    }
-}
-
 // Encode the staged rows [0, nrows) of a routed buffer: one thread per
 // (row, 32-block) -- four 128-bit shared loads, amax by packed u16 max, the
 // block scale(s), sixteen E2M1x2 conversions, one 16-byte code store and the
@@ -613,6 +582,7 @@ template <int MODE>
 __device__ __forceinline__ void encode_staged(const QuantParams& p, uint32_t sbuf, int stride, int row0,
                                               int nrows) {
     const int nb = p.Kbp >> 5;
+    const int katoms = p.katoms;
     const int tid = threadIdx.x;
     const float inv_nb = 1.0f / static_cast<float>(nb);
     for (int wi = tid; wi < nrows * nb; wi += blockDim.x) {
@@ -625,7 +595,30 @@ __device__ __forceinline__ void encode_staged(const QuantParams& p, uint32_t sbu
         const uint32_t src = sbuf + r * stride + b * QA_BLOCK_BYTES;
         const uint4 q0 = ptx::ld_shared_v4(src), q1 = ptx::ld_shared_v4(src + 16), q2 = ptx::ld_shared_v4(src + 32),
                     q3 = ptx::ld_shared_v4(src + 48);
-        encode_block<MODE>(p, t, b, q0, q1, q2, q3);
+        using mx::bf16x2_absmax;
+        const uint32_t m01 = bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(q0.x, q0.y), bf16x2_absmax(q0.z, q0.w)),
+                                           bf16x2_absmax(bf16x2_absmax(q1.x, q1.y), bf16x2_absmax(q1.z, q1.w)));
+        const uint32_t m23 = bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(q2.x, q2.y), bf16x2_absmax(q2.z, q2.w)),
+                                           bf16x2_absmax(bf16x2_absmax(q3.x, q3.y), bf16x2_absmax(q3.z, q3.w)));
+        uint8_t* codes = p.codes + static_cast<size_t>(t) * (p.Kbp >> 1) + b * 16;
+        if constexpr (MODE == QA_NV) {
+            float r_lo, r_hi;
+            const uint32_t s2 = mx::nv_block_scales(max(m01 & 0x7FFFu, (m01 >> 16) & 0x7FFFu),
+                                                    max(m23 & 0x7FFFu, (m23 >> 16) & 0x7FFFu), p.nv_k, p.nv_p2g,
+                                                    &r_lo, &r_hi);
+            *reinterpret_cast<uint4*>(codes) = make_uint4(encode8_words(q0, r_lo), encode8_words(q1, r_lo),
+                                                          encode8_words(q2, r_hi), encode8_words(q3, r_hi));
+            // 16-blocks 2b and 2b + 1: adjacent bytes of one atom row
+            *reinterpret_cast<uint16_t*>(p.scales + sf_offset(t, 2 * b, katoms)) = static_cast<uint16_t>(s2);
+        } else {
+            const uint32_t m = bf16x2_absmax(m01, m23);
+            const uint32_t amax = max(m & 0x7FFFu, (m >> 16) & 0x7FFFu);
+            float inv;
+            const int X = mx::bf16_block_exponent(amax, &inv);
+            *reinterpret_cast<uint4*>(codes) = make_uint4(encode8_words(q0, inv), encode8_words(q1, inv),
+                                                          encode8_words(q2, inv), encode8_words(q3, inv));
+            p.scales[sf_offset(t, b, katoms)] = static_cast<uint8_t>(b * 32 < p.Kb ? X + 127 : 0);
+        }
     }
     const int hv = p.kp >> 3;
     for (int i = tid; i < nrows * hv; i += blockDim.x) {
@@ -1164,11 +1157,13 @@ __global__ void __launch_bounds__(QA_THREADS) norm_quantize_kernel(QuantParams p
 //   and inv_s of the run in shared memory, read once for both rows -- and
 //   stores the 16-bit values at their routed places in the team's staged rows;
 //   then the team encodes the staged rows, a 32-block per lane at a time.
-// Staged rows are unpadded: the four 16-byte units of 32-block b stand in the
-// order u ^ ((b / 2) & 3), which makes the encoding's 128-bit reads by
-// consecutive lanes conflict-free; the lanes of a quarter warp store their
-// chunk's four words each starting from another one, for the same reason (the
-// order is laid out in the route table).
+// Staged rows are plain: bulk position p at byte 2p, the slots behind Kbp. A
+// lane stores its chunk's four words starting from the one that makes the
+// banks of lanes 8 apart differ (lanes next to one another differ by
+// themselves); the start is laid out in the route table, from the chunk's
+// address. In the encoding, lanes two blocks apart start their four 128-bit
+// reads from different units, which makes them conflict-free; the four code
+// words are put in order afterwards.
 // Two teams' worth of FP32 rows would not fit the registers: one row per team.
 constexpr int NQ_W = 2;  // warps per team
 
@@ -1192,6 +1187,44 @@ __device__ __forceinline__ void rotate_words(uint32_t (&w)[4], bool by1, bool by
     w[3] = by2 ? x1 : x3;
 }
 
+// One 32-block of row t from its 64 staged bytes at `src`: its maxima,
+// scale(s) and codes, with the four 16-byte units read from unit (b / 2) % 4 on, around the end.
+template <int MODE>
+__device__ __forceinline__ void encode_turned_block(const QuantParams& p, int t, int b, uint32_t src) {
+    const int turn = b >> 1;
+    uint4 q[4];
+    uint32_t m[4];  // packed maxima of the units, in the order read
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        q[i] = ptx::ld_shared_v4(src + ((i + turn) & 3) * 16);
+        m[i] = mx::bf16x2_absmax(mx::bf16x2_absmax(q[i].x, q[i].y), mx::bf16x2_absmax(q[i].z, q[i].w));
+    }
+    // unit u was read (u - turn)-th: turning 4 - turn places more puts them in order
+    const bool by1 = turn & 1, by2 = ((turn >> 1) ^ turn) & 1;  // bits of (-turn) & 3
+    uint32_t code[4];
+    uint8_t* codes = p.codes + static_cast<size_t>(t) * (p.Kbp >> 1) + b * 16;
+    if constexpr (MODE == QA_NV) {
+        uint32_t o[4] = {m[0], m[1], m[2], m[3]};
+        rotate_words(o, by1, by2);
+        const uint32_t lo = mx::bf16x2_absmax(o[0], o[1]), hi = mx::bf16x2_absmax(o[2], o[3]);
+        float r_lo, r_hi;
+        const uint32_t s2 = mx::nv_block_scales(max(lo & 0x7FFFu, (lo >> 16) & 0x7FFFu), max(hi & 0x7FFFu, (hi >> 16) & 0x7FFFu),
+                                                p.nv_k, p.nv_p2g, &r_lo, &r_hi);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) code[i] = encode8_words(q[i], ((i + turn) & 2) ? r_hi : r_lo);
+        *reinterpret_cast<uint16_t*>(p.scales + sf_offset(t, 2 * b, p.katoms)) = static_cast<uint16_t>(s2);
+    } else {
+        const uint32_t mm = mx::bf16x2_absmax(mx::bf16x2_absmax(m[0], m[1]), mx::bf16x2_absmax(m[2], m[3]));
+        float inv;
+        const int X = mx::bf16_block_exponent(max(mm & 0x7FFFu, (mm >> 16) & 0x7FFFu), &inv);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) code[i] = encode8_words(q[i], inv);
+        p.scales[sf_offset(t, b, p.katoms)] = static_cast<uint8_t>(b * 32 < p.Kb ? X + 127 : 0);
+    }
+    rotate_words(code, by1, by2);
+    *reinterpret_cast<uint4*>(codes) = make_uint4(code[0], code[1], code[2], code[3]);
+}
+
 template <int MODE, bool F32, int NS, int MINB>
 __global__ void __launch_bounds__(NormQuantShape<NS>::THREADS, MINB)
     norm_quantize_rows_kernel(QuantParams p, norm::Spec s, const void* X, uint32_t share, uint32_t tile_rows,
@@ -1211,22 +1244,26 @@ __global__ void __launch_bounds__(NormQuantShape<NS>::THREADS, MINB)
     const uint32_t stage = ptx::smem_u32(smem) + team * R * Shape::STRIDE;
     float* part = reinterpret_cast<float*>(smem + Shape::TEAMS * R * Shape::STRIDE) + team * 2 * R * W * NS;
     uint4* table = reinterpret_cast<uint4*>(smem + Shape::TEAMS * (R * Shape::STRIDE + 2 * R * W * NS * 4));
-    // words of chunk c: a, a, b, b (table[i * nchunk + c], i = 0..3), inv_s (4, 5), routes (6)
+    // words of chunk c: a, a, b, b (table[i * nchunk + c], i = 0..3), inv_s (4, 5), routes (6: staged bytes of the
+    // two columns of the word that is stored i-th; bits 14 and 15 of the first hold the number of that word)
 
     // staged byte of channel position `off` (an offset of the plan's route table)
     auto staged = [&](int off) -> uint32_t {
         if (off >= nb * QA_BLOCK_BYTES) return p.Kbp * 2 + (off - nb * QA_BLOCK_BYTES);
-        const int b = off / QA_BLOCK_BYTES, e = off - b * QA_BLOCK_BYTES;
-        return b * 64 + (((e >> 4) ^ (b >> 1)) & 3) * 16 + (e & 15);
+        const int b = off / QA_BLOCK_BYTES;
+        return b * 64 + (off - b * QA_BLOCK_BYTES);
     };
+    static_assert(Shape::STRIDE <= 1 << 14, "bits 14 and 15 of a staged byte are free");
     for (int c = tid; c < nchunk; c += Shape::THREADS) {
         const int2* rt = reinterpret_cast<const int2*>(p.route) + 4 * c;
         uint32_t word[4];
+        const uint32_t start = (((c & 31) >> 3) - (staged(__ldg(rt).x) >> 2)) & 3;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {  // the word that a lane stores i-th
-            const int2 dv = __ldg(rt + ((i + ((c & 31) >> 3)) & 3));
+        for (int i = 0; i < 4; ++i) {
+            const int2 dv = __ldg(rt + ((i + start) & 3));
             word[i] = staged(dv.x) | staged(dv.y) << 16;
         }
+        word[0] |= start << 14;
         table[6 * nchunk + c] = make_uint4(word[0], word[1], word[2], word[3]);
         table[4 * nchunk + c] = __ldg(reinterpret_cast<const uint4*>(p.inv_s) + 2 * c);
         table[5 * nchunk + c] = __ldg(reinterpret_cast<const uint4*>(p.inv_s) + 2 * c + 1);
@@ -1237,8 +1274,7 @@ __global__ void __launch_bounds__(NormQuantShape<NS>::THREADS, MINB)
         for (int i = tt; i < R * npad; i += 32 * W) {
             const int r = i / npad, c = i - r * npad;
             const int pos = p.Kb + c;
-            const uint32_t at = c < npb ? staged((pos >> 5) * QA_BLOCK_BYTES + (pos & 31) * 2)
-                                        : static_cast<uint32_t>(p.Kbp * 2 + (p.k + c - npb) * 2);
+            const uint32_t at = c < npb ? pos * 2 : p.Kbp * 2 + (p.k + c - npb) * 2;
             ptx::st_shared_u16(stage + r * Shape::STRIDE + at, 0);
         }
     }
@@ -1327,8 +1363,8 @@ __global__ void __launch_bounds__(NormQuantShape<NS>::THREADS, MINB)
                 const float2 ca[4] = {pair(a0.x, a0.y), pair(a0.z, a0.w), pair(a1.x, a1.y), pair(a1.z, a1.w)};
                 const float2 cb[4] = {pair(b0.x, b0.y), pair(b0.z, b0.w), pair(b1.x, b1.y), pair(b1.z, b1.w)};
                 const float2 cs[4] = {pair(s0.x, s0.y), pair(s0.z, s0.w), pair(s1.x, s1.y), pair(s1.z, s1.w)};
-                const uint32_t to[4] = {rt.x, rt.y, rt.z, rt.w};
-                const bool by1 = lane & 8, by2 = lane & 16;
+                const uint32_t to[4] = {rt.x & ~0xC000u, rt.y, rt.z, rt.w};
+                const bool by1 = rt.x & 0x4000u, by2 = rt.x & 0x8000u;
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     float2 v[4];
@@ -1339,7 +1375,7 @@ __global__ void __launch_bounds__(NormQuantShape<NS>::THREADS, MINB)
                         w[i] = norm_smooth2<false>(v[i], st[r], ca[i], cb[i], cs[i], 0u);
                         if constexpr (HPF) u[i] = norm_smooth2<true>(v[i], st[r], ca[i], cb[i], cs[i], 0xFFFFFFFFu);
                     }
-                    rotate_words(w, by1, by2);  // word i -> place i - lane / 8
+                    rotate_words(w, by1, by2);
                     if constexpr (HPF) {
                         rotate_words(u, by1, by2);
 #pragma unroll
@@ -1361,9 +1397,7 @@ __global__ void __launch_bounds__(NormQuantShape<NS>::THREADS, MINB)
             for (int i = tt; i < rows * nb; i += 32 * W) {
                 const int r = i >= nb, b = i - r * nb, row_r = static_cast<int>(row) + r;
                 const uint32_t src = stage + r * Shape::STRIDE + b * 64;
-                const int x = (b >> 1) & 3;
-                encode_block<MODE>(p, row_r, b, ptx::ld_shared_v4(src + x * 16), ptx::ld_shared_v4(src + (1 ^ x) * 16),
-                                   ptx::ld_shared_v4(src + (2 ^ x) * 16), ptx::ld_shared_v4(src + (3 ^ x) * 16));
+                encode_turned_block<MODE>(p, row_r, b, src);
             }
 #pragma unroll 1
             for (int i = 32 * W - 1 - tt; i < rows * hv; i += 32 * W) {
