@@ -1165,16 +1165,15 @@ __global__ void __launch_bounds__(QA_THREADS) norm_quantize_kernel(QuantParams p
 // reads from different units, which makes them conflict-free; the four code
 // words are put in order afterwards.
 // Two teams' worth of FP32 rows would not fit the registers: one row per team.
-constexpr int NQ_W = 2;  // warps per team
 
-template <int NS>
+template <int W, int NS>
 struct NormQuantShape {
-    static constexpr int COLS = NQ_W * NS * norm::SEG;         // widest row
+    static constexpr int COLS = W * NS * norm::SEG;            // widest row
     static constexpr int STRIDE = 2 * (COLS + 128 + 64);       // bytes of one staged row (Kbp + kp <= K + 192)
-    static constexpr int TEAMS = NS > 4 ? 7 : 8;
-    static constexpr int THREADS = 32 * NQ_W * TEAMS;
+    static constexpr int TEAMS = COLS > 1024 ? 24 / W : 16 / W;
+    static constexpr int THREADS = 32 * W * TEAMS;
     static constexpr int smem(int K, int R) {
-        return TEAMS * (R * STRIDE + 2 * R * NQ_W * NS * 4) + (K / norm::CHUNK) * 7 * 16;
+        return TEAMS * (R * STRIDE + 2 * R * W * NS * 4) + (K / norm::CHUNK) * 7 * 16;
     }
 };
 
@@ -1225,15 +1224,14 @@ __device__ __forceinline__ void encode_turned_block(const QuantParams& p, int t,
     *reinterpret_cast<uint4*>(codes) = make_uint4(code[0], code[1], code[2], code[3]);
 }
 
-template <int MODE, bool F32, int NS, int MINB>
-__global__ void __launch_bounds__(NormQuantShape<NS>::THREADS, MINB)
+template <int MODE, bool F32, int W, int NS, int MINB>
+__global__ void __launch_bounds__(NormQuantShape<W, NS>::THREADS, MINB)
     norm_quantize_rows_kernel(QuantParams p, norm::Spec s, const void* X, uint32_t share, uint32_t tile_rows,
                               uint32_t tiles_per_run, uint32_t tiles) {
-    using Shape = NormQuantShape<NS>;
+    using Shape = NormQuantShape<W, NS>;
     constexpr bool HPF = MODE == QA_MX_F16;
     constexpr int R = F32 ? 1 : 2;
     constexpr int XQ = F32 ? 2 : 1;
-    constexpr int W = NQ_W;
     ptx::grid_dep_launch();  // the dual_gemm that follows may start its prologue
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, team = warp / W, j = warp % W, tt = tid % (32 * W);
@@ -1587,19 +1585,19 @@ static QuantParams quant_params(const osm_plan* pl, const uint16_t* X, int64_t M
                   pow2f(-pl->g_act)};
 }
 
-template <int NS, int MINB>
+template <int W, int NS, int MINB>
 static int launch_norm_quantize_rows(const QuantParams& p, int mode, const norm::Spec& s, const void* X, bool f32, int64_t M,
                                      int64_t run, cudaStream_t st) {
     auto pick = [&](auto f) {
         constexpr bool F = decltype(f)::value;
-        return mode == QA_NV ? norm_quantize_rows_kernel<QA_NV, F, NS, MINB>
-                             : (mode == QA_MX_F16 ? norm_quantize_rows_kernel<QA_MX_F16, F, NS, MINB>
-                                                  : norm_quantize_rows_kernel<QA_MX, F, NS, MINB>);
+        return mode == QA_NV ? norm_quantize_rows_kernel<QA_NV, F, W, NS, MINB>
+                             : (mode == QA_MX_F16 ? norm_quantize_rows_kernel<QA_MX_F16, F, W, NS, MINB>
+                                                  : norm_quantize_rows_kernel<QA_MX, F, W, NS, MINB>);
     };
     auto kern = f32 ? pick(std::true_type{}) : pick(std::false_type{});
-    const size_t smem = NormQuantShape<NS>::smem(p.K, f32 ? 1 : 2);
+    const size_t smem = NormQuantShape<W, NS>::smem(p.K, f32 ? 1 : 2);
     int per_sm = 0, sms = 0;
-    int rc = prepare_kernel(reinterpret_cast<const void*>(kern), NormQuantShape<NS>::THREADS, smem, &per_sm, &sms);
+    int rc = prepare_kernel(reinterpret_cast<const void*>(kern), NormQuantShape<W, NS>::THREADS, smem, &per_sm, &sms);
     if (rc) return rc;
     if (per_sm < 1) return fail(OSM_ERR_UNSUPPORTED, "norm_quantize_act: no CTA fits (K = %d)", p.K);
     // one tile per CTA: each run is cut into its part of them
@@ -1607,7 +1605,7 @@ static int launch_norm_quantize_rows(const QuantParams& p, int mode, const norm:
     const int64_t cuts = ctas * run / M > 1 ? ctas * run / M : 1;
     const int64_t tile_rows = ceil_div(run, cuts), per_run = ceil_div(run, tile_rows);
     const int64_t tiles = ceil_div(M, run) * per_run;
-    kern<<<static_cast<unsigned>(tiles < ctas ? tiles : ctas), NormQuantShape<NS>::THREADS, smem, st>>>(
+    kern<<<static_cast<unsigned>(tiles < ctas ? tiles : ctas), NormQuantShape<W, NS>::THREADS, smem, st>>>(
         p, s, X, static_cast<uint32_t>(run), static_cast<uint32_t>(tile_rows), static_cast<uint32_t>(per_run),
         static_cast<uint32_t>(tiles));
     return check_cuda(cudaGetLastError(), "norm_quantize_act launch");
@@ -1625,8 +1623,8 @@ int launch_norm_quantize(const osm_plan* pl, const void* X, int x_dtype, int64_t
     // Many rows: teams of warps (see norm_quantize_rows_kernel). Below about
     // eight rows per SM its tables cost more than they save.
     if (pl->K <= 5120 && run >= 64 && M >= 148 * 8) {
-        if (pl->K <= 1024) return launch_norm_quantize_rows<2, 2>(p, mode, s, X, f32, M, run, st);
-        return launch_norm_quantize_rows<10, 1>(p, mode, s, X, f32, M, run, st);
+        if (pl->K <= 1024) return launch_norm_quantize_rows<2, 2, 2>(p, mode, s, X, f32, M, run, st);
+        return launch_norm_quantize_rows<4, 5, 1>(p, mode, s, X, f32, M, run, st);
     }
     const size_t smem = ((2 * nseg * 4 + 15) & ~15) + qa_row_stride(static_cast<int>(pl->Kbp / 32), static_cast<int>(pl->kp));
     auto pick = [&](auto f) {
