@@ -78,8 +78,11 @@ static_assert((LAUNCH_REGS - CTRL_REGS) * 128 >= (EPI_REGS - LAUNCH_REGS) * 256,
 static_assert(CTRL_REGS + 2 * EPI_REGS <= 512, "register split exceeds a sub-partition");
 static_assert(LAUNCH_REGS * 3 <= 512 && CTRL_REGS % 8 == 0 && EPI_REGS % 8 == 0, "register counts");
 // Each epilogue kind is its own kernel instantiation with its own register
-// allocation; only the FFN requantisation needs more than LAUNCH_REGS.
-__host__ __device__ constexpr bool uses_register_split(int epi) { return epi == OSM_EPI_GELU_REQUANT; }
+// allocation; the FFN requantisation and the residual sum (which holds the
+// residual's words beside the accumulators) need more than LAUNCH_REGS.
+__host__ __device__ constexpr bool uses_register_split(int epi) {
+    return epi == OSM_EPI_GELU_REQUANT || epi == EPI_ONTO_BF16 || epi == EPI_ONTO_F32;
+}
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t SF_COL0 = 256;       // scale factors live after the accumulator
 // Tile raster. When the packed weights fit comfortably in L2 (the FFN
@@ -254,70 +257,77 @@ __device__ __forceinline__ void store_slab(const GemmParams& p, int64_t row0, in
         }
     }
 }
-// EPI_ONTO_*: Y = r + gate * (acc + bias) for one slab, laid out as in
-// store_slab. The residual words of B column blocks are loaded before the
-// first of them is used, so that their latencies overlap; a thread reads
+// EPI_ONTO_*: Y = r + gate * (acc + bias), laid out as in store_slab. The
+// residual words of a slab (`w`: rows ra and rb of each of the 16 column
+// blocks) are in registers before its accumulator: those of a tile's first
+// slab are loaded while the MMAs still run, those of the second as the first
+// one's are used up, so their latency is hidden. (Loading them in the store
+// loop doubled the time at 4096 x 5120 x 5120: 104 -> 201 us.) A thread reads
 // each word of r before it writes the same word of Y, so Y may be r. The
 // product is gated and added in FP32 and rounded once, to the stream's type.
-template <int EPI, bool NV>
-__device__ __forceinline__ void onto_slab(const GemmParams& p, int64_t row0, int64_t col0, int lane, const uint32_t* r) {
-    constexpr bool F32 = EPI == EPI_ONTO_F32;
-    constexpr int B = F32 ? 4 : 8;
+template <bool F32>
+struct Residual {
+    using Word = typename std::conditional<F32, float2, uint32_t>::type;
+    Word w[32];
+    // the words of the slab of rows row0 .. row0 + 15
+    __device__ __forceinline__ const Word* row_ptr(const void* base, const GemmParams& p, int64_t row, int64_t col0, int lane) const {
+        return static_cast<const Word*>(base) + row * (p.N >> 1) + (col0 >> 1) + (lane & 3);
+    }
+    __device__ __forceinline__ void load(const GemmParams& p, int64_t row0, int64_t col0, int lane, int nj) {
+        const int64_t ra = row0 + (lane >> 2), rb = ra + 8;
+        const Word *pa = row_ptr(p.onto.r, p, ra, col0, lane), *pb = row_ptr(p.onto.r, p, rb, col0, lane);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            if (j < nj && ra < p.M) w[2 * j] = pa[4 * j];
+            if (j < nj && rb < p.M) w[2 * j + 1] = pb[4 * j];
+        }
+    }
+};
+template <bool F32, bool NV>
+__device__ __forceinline__ void onto_slab(const GemmParams& p, int64_t row0, int64_t col0, int lane, int nj, const uint32_t* r,
+                                          Residual<F32>& res, bool more) {
+    using Word = typename Residual<F32>::Word;
     const int64_t ra = row0 + (lane >> 2), rb = ra + 8;
-    const int cq = 2 * (lane & 3);
-    const bool on_a = ra < p.M, on_b = rb < p.M;
+    const bool on_a = ra < p.M, on_b = rb < p.M, next_a = more && ra + 16 < p.M, next_b = more && rb + 16 < p.M;
+    const int64_t c0 = col0 + 2 * (lane & 3);
     const float *gate_a = nullptr, *gate_b = nullptr;
     if (p.onto.gate) {  // rows past M read the last row's gate
         const uint32_t last = static_cast<uint32_t>(p.M - 1), share = static_cast<uint32_t>(p.onto.gate_rows);
-        gate_a = p.onto.gate + (min(static_cast<uint32_t>(ra), last) / share) * p.onto.gate_stride;
-        gate_b = p.onto.gate + (min(static_cast<uint32_t>(rb), last) / share) * p.onto.gate_stride;
+        gate_a = p.onto.gate + (min(static_cast<uint32_t>(ra), last) / share) * p.onto.gate_stride + c0;
+        gate_b = p.onto.gate + (min(static_cast<uint32_t>(rb), last) / share) * p.onto.gate_stride + c0;
     }
-    using Word = typename std::conditional<F32, float2, uint32_t>::type;
-    const Word* res = static_cast<const Word*>(p.onto.r);
-    Word* out = static_cast<Word*>(p.Y);
-    const int64_t ia = ra * (p.N >> 1), ib = rb * (p.N >> 1);
-#pragma unroll
-    for (int j0 = 0; j0 < 16; j0 += B) {
-        Word wa[B], wb[B];
-#pragma unroll
-        for (int i = 0; i < B; ++i) {
-            const int64_t col = col0 + 8 * (j0 + i) + cq;
-            if (col < p.N) {
-                if (on_a) wa[i] = res[ia + (col >> 1)];
-                if (on_b) wb[i] = res[ib + (col >> 1)];
-            }
+    const Word *na = res.row_ptr(p.onto.r, p, ra + 16, col0, lane), *nb = res.row_ptr(p.onto.r, p, rb + 16, col0, lane);
+    Word *oa = const_cast<Word*>(res.row_ptr(p.Y, p, ra, col0, lane)), *ob = const_cast<Word*>(res.row_ptr(p.Y, p, rb, col0, lane));
+    auto sum = [](float2 v, Word w) -> Word {
+        if constexpr (F32) {
+            return __fadd2_rn(w, v);
+        } else {
+            v = __fadd2_rn(make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)), v);
+            return mx::bf16x2_bits(v.x, v.y);
         }
+    };
 #pragma unroll
-        for (int i = 0; i < B; ++i) {
-            const int j = j0 + i;
-            const int64_t col = col0 + 8 * j + cq;
-            if (col >= p.N) break;
-            float2 a = make_float2(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]));
-            float2 b = make_float2(__uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
-            if constexpr (NV) {
-                a = __fmul2_rn(a, make_float2(p.out_scale, p.out_scale));
-                b = __fmul2_rn(b, make_float2(p.out_scale, p.out_scale));
-            }
-            if (p.bias) {
-                const float2 bb = __ldg(reinterpret_cast<const float2*>(p.bias + col));
-                a = __fadd2_rn(a, bb);
-                b = __fadd2_rn(b, bb);
-            }
-            if (p.onto.gate) {
-                a = __fmul2_rn(a, __ldg(reinterpret_cast<const float2*>(gate_a + col)));
-                b = __fmul2_rn(b, __ldg(reinterpret_cast<const float2*>(gate_b + col)));
-            }
-            auto add = [](float2 v, Word w) {
-                if constexpr (F32) return __fadd2_rn(w, v);
-                else return __fadd2_rn(make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)), v);
-            };
-            auto put = [&](int64_t at, float2 v) {
-                if constexpr (F32) out[at + (col >> 1)] = v;
-                else out[at + (col >> 1)] = mx::bf16x2_bits(v.x, v.y);
-            };
-            if (on_a) put(ia, add(a, wa[i]));
-            if (on_b) put(ib, add(b, wb[i]));
+    for (int j = 0; j < 16; ++j) {
+        if (j >= nj) break;
+        float2 a = make_float2(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]));
+        float2 b = make_float2(__uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
+        if constexpr (NV) {
+            a = __fmul2_rn(a, make_float2(p.out_scale, p.out_scale));
+            b = __fmul2_rn(b, make_float2(p.out_scale, p.out_scale));
         }
+        if (p.bias) {
+            const float2 bb = __ldg(reinterpret_cast<const float2*>(p.bias + c0 + 8 * j));
+            a = __fadd2_rn(a, bb);
+            b = __fadd2_rn(b, bb);
+        }
+        if (p.onto.gate) {
+            a = __fmul2_rn(a, __ldg(reinterpret_cast<const float2*>(gate_a + 8 * j)));
+            b = __fmul2_rn(b, __ldg(reinterpret_cast<const float2*>(gate_b + 8 * j)));
+        }
+        if (on_a) oa[4 * j] = sum(a, res.w[2 * j]);
+        if (on_b) ob[4 * j] = sum(b, res.w[2 * j + 1]);
+        if (next_a) res.w[2 * j] = na[4 * j];
+        if (next_b) res.w[2 * j + 1] = nb[4 * j];
     }
 }
 // Bring a warp's part of the residual tile (32 rows x 128 columns) into L2
@@ -634,9 +644,15 @@ __device__ __forceinline__ void epilogue_role(const GemmParams& p, Smem<NV>& S, 
     for (int tile = pair; tile < tiles; tile += npairs) {
         int m_blk, n_blk;
         tile_coords(tile, p.num_m, p.num_n, p.group_m, m_blk, n_blk);
-        if constexpr (EPI == EPI_ONTO_BF16 || EPI == EPI_ONTO_F32)
-            prefetch_residual<EPI == EPI_ONTO_F32>(p, (int64_t)m_blk * 2 * BM + (int64_t)rank * BM + q * 32,
-                                                   (int64_t)n_blk * BN + half * 128, lane);
+        const int64_t y0 = (int64_t)m_blk * 2 * BM + (int64_t)rank * BM + q * 32;
+        const int64_t x0 = (int64_t)n_blk * BN + half * 128;
+        constexpr bool ONTO = EPI == EPI_ONTO_BF16 || EPI == EPI_ONTO_F32;
+        Residual<EPI == EPI_ONTO_F32> res;
+        const int nj = static_cast<int>(min(static_cast<int64_t>(16), (p.N - x0) >> 3));  // column blocks (N % 32 == 0)
+        if constexpr (ONTO) {
+            prefetch_residual<EPI == EPI_ONTO_F32>(p, y0, x0, lane);
+            res.load(p, y0, x0, lane, nj);
+        }
         int ok = 1;
         if (lane == 0)
             // the accumulator completes once per tile (about 10 us of MMAs):
@@ -651,8 +667,6 @@ __device__ __forceinline__ void epilogue_role(const GemmParams& p, Smem<NV>& S, 
         }
         ptx::tc_fence_after();
         const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + half * 128;
-        const int64_t y0 = (int64_t)m_blk * 2 * BM + (int64_t)rank * BM + q * 32;
-        const int64_t x0 = (int64_t)n_blk * BN + half * 128;
         if constexpr (EPI == OSM_EPI_GELU_REQUANT) {
             static_assert(!NV, "the fused requantisation takes MXFP4 operands");
             // lane = row, 32 consecutive columns per load: whole MX blocks per lane
@@ -677,8 +691,7 @@ __device__ __forceinline__ void epilogue_role(const GemmParams& p, Smem<NV>& S, 
             if (x0 < p.N) {
 #pragma unroll 1
                 for (int sl = 0; sl < 2; ++sl) {
-                    if constexpr (EPI == EPI_ONTO_BF16 || EPI == EPI_ONTO_F32)
-                        onto_slab<EPI, NV>(p, y0 + 16 * sl, x0, lane, r);
+                    if constexpr (ONTO) onto_slab<EPI == EPI_ONTO_F32, NV>(p, y0 + 16 * sl, x0, lane, nj, r, res, sl == 0);
                     else
                         store_slab<EPI, NV>(p, y0 + 16 * sl, x0, lane, r);
                     shift_down<64>(r);
