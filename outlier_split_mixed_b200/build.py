@@ -17,7 +17,7 @@ LIB = os.path.join(PKG, "libosm.so")
 
 SOURCES = ["osm_api.cu", "osm_quant.cu", "osm_gemm.cu", "osm_noalloc.cu", "osm_refresh.cu", "osm_norm.cu", "osm_linear.cu",
            "osm_block.cu"]
-HEADERS = ["osm_internal.h", "osm_ptx.cuh", "osm_mx.cuh", "osm_norm.cuh"]
+HEADERS = ["osm_internal.h", "osm_ptx.cuh", "osm_mx.cuh", "osm_norm.cuh", "osm_onto.cuh"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-gencode", "arch=compute_100a,code=sm_100a",

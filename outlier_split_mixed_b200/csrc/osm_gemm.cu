@@ -46,10 +46,10 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
-#include <type_traits>
 
 #include "osm_internal.h"
 #include "osm_mx.cuh"
+#include "osm_onto.cuh"
 #include "osm_ptx.cuh"
 
 namespace osm {
@@ -172,7 +172,7 @@ struct GemmParams {
     int nKb, nKbp, nk, nkp;   // next's bulk / outlier widths
     int next_hp_fp16;         // next's outlier slots in binary16
     int64_t m_pad;            // M rounded up to 128 (rows of next_scales)
-    Onto onto;                // EPI_ONTO_*: the residual stream and its gate
+    onto::Params onto;        // EPI_ONTO_*: the end of the product
 };
 
 __device__ __forceinline__ void tile_coords(int tile, int num_m, int num_n, int group_m, int& m_blk, int& n_blk) {
@@ -256,90 +256,6 @@ __device__ __forceinline__ void store_slab(const GemmParams& p, int64_t row0, in
             if (rb < p.M) *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.Y) + rb * p.N + col) = mx::bf16x2_bits(b.x, b.y);
         }
     }
-}
-// EPI_ONTO_*: Y = r + gate * (acc + bias), laid out as in store_slab. The
-// residual words of a slab (`w`: rows ra and rb of each of the 16 column
-// blocks) are in registers before its accumulator: those of a tile's first
-// slab are loaded while the MMAs still run, those of the second as the first
-// one's are used up, so their latency is hidden. (Loading them in the store
-// loop doubled the time at 4096 x 5120 x 5120: 104 -> 201 us.) A thread reads
-// each word of r before it writes the same word of Y, so Y may be r. The
-// product is gated and added in FP32 and rounded once, to the stream's type.
-template <bool F32>
-struct Residual {
-    using Word = typename std::conditional<F32, float2, uint32_t>::type;
-    Word w[32];
-    // the words of the slab of rows row0 .. row0 + 15
-    __device__ __forceinline__ const Word* row_ptr(const void* base, const GemmParams& p, int64_t row, int64_t col0, int lane) const {
-        return static_cast<const Word*>(base) + row * (p.N >> 1) + (col0 >> 1) + (lane & 3);
-    }
-    __device__ __forceinline__ void load(const GemmParams& p, int64_t row0, int64_t col0, int lane, int nj) {
-        const int64_t ra = row0 + (lane >> 2), rb = ra + 8;
-        const Word *pa = row_ptr(p.onto.r, p, ra, col0, lane), *pb = row_ptr(p.onto.r, p, rb, col0, lane);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            if (j < nj && ra < p.M) w[2 * j] = pa[4 * j];
-            if (j < nj && rb < p.M) w[2 * j + 1] = pb[4 * j];
-        }
-    }
-};
-template <bool F32, bool NV>
-__device__ __forceinline__ void onto_slab(const GemmParams& p, int64_t row0, int64_t col0, int lane, int nj, const uint32_t* r,
-                                          Residual<F32>& res, bool more) {
-    using Word = typename Residual<F32>::Word;
-    const int64_t ra = row0 + (lane >> 2), rb = ra + 8;
-    const bool on_a = ra < p.M, on_b = rb < p.M, next_a = more && ra + 16 < p.M, next_b = more && rb + 16 < p.M;
-    const int64_t c0 = col0 + 2 * (lane & 3);
-    const float *gate_a = nullptr, *gate_b = nullptr;
-    if (p.onto.gate) {  // rows past M read the last row's gate
-        const uint32_t last = static_cast<uint32_t>(p.M - 1), share = static_cast<uint32_t>(p.onto.gate_rows);
-        gate_a = p.onto.gate + (min(static_cast<uint32_t>(ra), last) / share) * p.onto.gate_stride + c0;
-        gate_b = p.onto.gate + (min(static_cast<uint32_t>(rb), last) / share) * p.onto.gate_stride + c0;
-    }
-    const Word *na = res.row_ptr(p.onto.r, p, ra + 16, col0, lane), *nb = res.row_ptr(p.onto.r, p, rb + 16, col0, lane);
-    Word *oa = const_cast<Word*>(res.row_ptr(p.Y, p, ra, col0, lane)), *ob = const_cast<Word*>(res.row_ptr(p.Y, p, rb, col0, lane));
-    auto sum = [](float2 v, Word w) -> Word {
-        if constexpr (F32) {
-            return __fadd2_rn(w, v);
-        } else {
-            v = __fadd2_rn(make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)), v);
-            return mx::bf16x2_bits(v.x, v.y);
-        }
-    };
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        if (j >= nj) break;
-        float2 a = make_float2(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]));
-        float2 b = make_float2(__uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
-        if constexpr (NV) {
-            a = __fmul2_rn(a, make_float2(p.out_scale, p.out_scale));
-            b = __fmul2_rn(b, make_float2(p.out_scale, p.out_scale));
-        }
-        if (p.bias) {
-            const float2 bb = __ldg(reinterpret_cast<const float2*>(p.bias + c0 + 8 * j));
-            a = __fadd2_rn(a, bb);
-            b = __fadd2_rn(b, bb);
-        }
-        if (p.onto.gate) {
-            a = __fmul2_rn(a, __ldg(reinterpret_cast<const float2*>(gate_a + 8 * j)));
-            b = __fmul2_rn(b, __ldg(reinterpret_cast<const float2*>(gate_b + 8 * j)));
-        }
-        if (on_a) oa[4 * j] = sum(a, res.w[2 * j]);
-        if (on_b) ob[4 * j] = sum(b, res.w[2 * j + 1]);
-        if (next_a) res.w[2 * j] = na[4 * j];
-        if (next_b) res.w[2 * j + 1] = nb[4 * j];
-    }
-}
-// Bring a warp's part of the residual tile (32 rows x 128 columns) into L2
-// while its accumulator is still being computed.
-template <bool F32>
-__device__ __forceinline__ void prefetch_residual(const GemmParams& p, int64_t y0, int64_t x0, int lane) {
-    const int64_t row = y0 + lane;
-    if (row >= p.M || x0 >= p.N) return;
-    constexpr int W = F32 ? 4 : 2;
-    const char* at = static_cast<const char*>(p.onto.r) + (row * p.N + x0) * W;
-    const int bytes = static_cast<int>(min(static_cast<int64_t>(128), p.N - x0)) * W;
-    for (int o = 0; o < bytes; o += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + o));
 }
 // Wait for this warp's tensor-memory loads, then tell the leader CTA's
 // MMA warp that the accumulator may be overwritten (16 arrivals: 8 warps in
@@ -631,6 +547,13 @@ __device__ __forceinline__ void mma_role(const GemmParams& p, Smem<NV>& S, bool 
     }
 }
 
+// A warp's staged bias and gate (shared memory of the EPI_ONTO_* kernels alone).
+template <int EPI>
+__device__ __forceinline__ onto::Vectors& epilogue_vectors(int warp) {
+    __shared__ onto::Vectors vectors[NUM_EPI_WARPS];
+    return vectors[warp];
+}
+
 // Epilogue, warps 0..7 of both CTAs: drain the accumulator, release
 // it to the MMA issuer, then convert and store.
 template <int EPI, bool NV>
@@ -641,17 +564,18 @@ __device__ __forceinline__ void epilogue_role(const GemmParams& p, Smem<NV>& S, 
     const int half = warp >> 2;  // columns [128*half, 128*half + 128) of the tile
     const uint32_t acc_empty_leader = ptx::mapa(ptx::smem_u32(&S.acc_empty), 0);
     uint32_t acc_phase = 0;
+    constexpr bool ONTO = EPI == EPI_ONTO_BF16 || EPI == EPI_ONTO_F32;
+    onto::Tile<EPI == EPI_ONTO_F32> end;
+    onto::Vectors* vectors = nullptr;
+    if constexpr (ONTO) vectors = &epilogue_vectors<EPI>(warp);
     for (int tile = pair; tile < tiles; tile += npairs) {
         int m_blk, n_blk;
         tile_coords(tile, p.num_m, p.num_n, p.group_m, m_blk, n_blk);
         const int64_t y0 = (int64_t)m_blk * 2 * BM + (int64_t)rank * BM + q * 32;
         const int64_t x0 = (int64_t)n_blk * BN + half * 128;
-        constexpr bool ONTO = EPI == EPI_ONTO_BF16 || EPI == EPI_ONTO_F32;
-        Residual<EPI == EPI_ONTO_F32> res;
-        const int nj = static_cast<int>(min(static_cast<int64_t>(16), (p.N - x0) >> 3));  // column blocks (N % 32 == 0)
         if constexpr (ONTO) {
-            prefetch_residual<EPI == EPI_ONTO_F32>(p, y0, x0, lane);
-            res.load(p, y0, x0, lane, nj);
+            end.prepare(p.onto, y0, x0, lane, *vectors);
+            end.load_first(p.onto, lane);
         }
         int ok = 1;
         if (lane == 0)
@@ -691,7 +615,7 @@ __device__ __forceinline__ void epilogue_role(const GemmParams& p, Smem<NV>& S, 
             if (x0 < p.N) {
 #pragma unroll 1
                 for (int sl = 0; sl < 2; ++sl) {
-                    if constexpr (ONTO) onto_slab<EPI == EPI_ONTO_F32, NV>(p, y0 + 16 * sl, x0, lane, nj, r, res, sl == 0);
+                    if constexpr (ONTO) end.template store<NV, false>(p.onto, sl, lane, *vectors, r);
                     else
                         store_slab<EPI, NV>(p, y0 + 16 * sl, x0, lane, r);
                     shift_down<64>(r);
@@ -894,7 +818,7 @@ int launch_dual_gemm(const osm_plan* pl, const uint8_t* a_codes, const uint8_t* 
     }
     p.n_row_tiles = static_cast<int>(ceil_div(pl->N, 128));
     p.epi = epi;
-    if (onto) p.onto = *onto;
+    if (onto) p.onto = onto::Params{M, pl->N, bias, Y, *onto, nv ? pow2f(pl->g_act + pl->g_w) : 1.0f, OSM_ACT_NONE};
     p.idesc_hp = pl->hp_fp16 ? IDESC_F16 : IDESC_BF16;
     p.out_scale = nv ? pow2f(pl->g_act + pl->g_w) : 1.0f;
     if (epi == OSM_EPI_GELU_REQUANT) {

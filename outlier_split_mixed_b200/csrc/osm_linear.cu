@@ -23,10 +23,10 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
-#include <type_traits>
 
 #include "osm_internal.h"
 #include "osm_mx.cuh"
+#include "osm_onto.cuh"
 #include "osm_ptx.cuh"
 
 namespace osm {
@@ -40,14 +40,10 @@ constexpr uint16_t PAIR_MASK = 0x3;
 struct LinearParams {
     CUtensorMap tm_x;    // X    [M][K] bf16
     CUtensorMap tm_w;    // w_hp [N][kp] bf16, box 64 x 128
-    const float* bias;
-    void* Y;
-    Onto onto;
+    onto::Params end;    // sizes and the end of the product
     uint32_t* status;
     uint64_t wait_limit_ns;
-    int64_t M, N;
     int ksteps;
-    int act;
     int num_m, num_n, group_m;  // pair_kernel: tiles and raster
 };
 
@@ -61,24 +57,24 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
     return ptx::smem_desc(saddr, 16, 1024, ptx::LAYOUT_SW128);
 }
 
-// x / (1 + 2^z) with z = -x log2(e); z is capped so that 1 + 2^z stays finite.
-__device__ __forceinline__ float2 silu2(float2 x) {
-    const float2 z = __fmul2_rn(x, make_float2(-1.44269504f, -1.44269504f));
-    const float2 d = __fadd2_rn(make_float2(mx::ex2_approx(fminf(z.x, 126.0f)), mx::ex2_approx(fminf(z.y, 126.0f))),
-                                make_float2(1.0f, 1.0f));
-    return __fmul2_rn(x, make_float2(mx::rcp_approx(d.x), mx::rcp_approx(d.y)));
-}
-__device__ __forceinline__ float2 activate2(float2 v, int act) {
-    if (act == OSM_ACT_GELU) return mx::gelu2(v);
-    if (act == OSM_ACT_SILU) return silu2(v);
-    return v;
-}
+// The tensor cores round the accumulator toward zero at every 16 values of K;
+// the errors have one sign, so they grow with K (1.6e-5 of the result at K =
+// 13824, where FP32 sums rounded to nearest are within 1.5e-6). A BF16 result
+// does not see them. For an FP32 result the products of FP32_CHUNK K-steps are
+// one sum in tensor memory, and the chunks' sums are added up in registers,
+// rounded to nearest, while the MMAs of the next chunk run.
+constexpr int FP32_CHUNK = 8;  // K-steps: 512 values, 32 roundings
 
 // ------------------------------------------------------------ pair_kernel
 
 constexpr int PK_STAGES = 6;
 constexpr int PK_EPI_WARPS = 8;
-constexpr int PK_THREADS = 32 * PK_EPI_WARPS + 64;
+// Warpgroup 2 holds the producer and the MMA issuer and gives registers back
+// to the epilogue (an FP32 tile's 128 sums, 64 residual words and the slab
+// being read); 384 x 168 registers are launched (see osm_gemm.cu).
+constexpr int PK_THREADS = 32 * PK_EPI_WARPS + 128;
+constexpr int PK_LAUNCH_REGS = 168, PK_CTRL_REGS = 56, PK_EPI_REGS = 224;
+static_assert((PK_LAUNCH_REGS - PK_CTRL_REGS) * 128 >= (PK_EPI_REGS - PK_LAUNCH_REGS) * 256, "register split exceeds the launch");
 constexpr int PK_PRODUCER = PK_EPI_WARPS, PK_MMA = PK_EPI_WARPS + 1;
 constexpr int PK_N = 256;
 constexpr uint32_t PK_IDESC = idesc_bf16(256, PK_N);
@@ -88,8 +84,9 @@ struct __align__(1024) PairSmem {
     uint8_t b[PK_STAGES][TILE];  // this CTA's half of the 256 output channels
     uint64_t full[PK_STAGES];    // leader: all copies of both CTAs for the slot have landed
     uint64_t empty[PK_STAGES];   // both: the MMAs reading the slot have completed
-    uint64_t acc_full[2];        // both: an accumulator is complete
+    uint64_t acc_full[2];        // both: an accumulator is complete (a tile's, or an FP32 chunk's)
     uint64_t acc_empty[2];       // leader: both CTAs have drained it
+    onto::Vectors vectors[PK_EPI_WARPS];
     uint64_t drain;
     uint32_t tmem_base;
     int abort_flag;
@@ -129,81 +126,17 @@ __device__ __forceinline__ void tmem_ld_16x256b_x16(uint32_t taddr, uint32_t* r)
         : "r"(taddr));
 }
 
-// Epilogue of one 16-row x 128-column slab. The residual words of B column
-// blocks are loaded before the first is used; a thread reads each word of R
-// before it writes the same word of Y, so Y may be R. FP32 until the one
-// rounding to Y's type.
-template <bool F32>
-__device__ __forceinline__ void pair_slab(const LinearParams& p, int64_t row0, int64_t col0, int lane, const uint32_t* r) {
-    constexpr int B = F32 ? 4 : 8;
-    const int64_t ra = row0 + (lane >> 2), rb = ra + 8;
-    const int cq = 2 * (lane & 3);
-    const bool on_a = ra < p.M, on_b = rb < p.M;
-    const float *gate_a = nullptr, *gate_b = nullptr;
-    if (p.onto.gate) {  // rows past M read the last row's gate
-        const uint32_t last = static_cast<uint32_t>(p.M - 1), share = static_cast<uint32_t>(p.onto.gate_rows);
-        gate_a = p.onto.gate + (min(static_cast<uint32_t>(ra), last) / share) * p.onto.gate_stride;
-        gate_b = p.onto.gate + (min(static_cast<uint32_t>(rb), last) / share) * p.onto.gate_stride;
-    }
-    using Word = typename std::conditional<F32, float2, uint32_t>::type;
-    const Word* res = static_cast<const Word*>(p.onto.r);
-    Word* out = static_cast<Word*>(p.Y);
-    const int64_t ia = ra * (p.N >> 1), ib = rb * (p.N >> 1);
-#pragma unroll
-    for (int j0 = 0; j0 < 16; j0 += B) {
-        Word wa[B], wb[B];
-        if (res) {
-#pragma unroll
-            for (int i = 0; i < B; ++i) {
-                const int64_t col = col0 + 8 * (j0 + i) + cq;
-                if (col < p.N) {
-                    if (on_a) wa[i] = res[ia + (col >> 1)];
-                    if (on_b) wb[i] = res[ib + (col >> 1)];
-                }
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < B; ++i) {
-            const int j = j0 + i;
-            const int64_t col = col0 + 8 * j + cq;
-            if (col >= p.N) break;
-            float2 a = make_float2(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]));
-            float2 b = make_float2(__uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
-            if (p.bias) {
-                const float2 bb = __ldg(reinterpret_cast<const float2*>(p.bias + col));
-                a = __fadd2_rn(a, bb);
-                b = __fadd2_rn(b, bb);
-            }
-            a = activate2(a, p.act);
-            b = activate2(b, p.act);
-            if (p.onto.gate) {
-                a = __fmul2_rn(a, __ldg(reinterpret_cast<const float2*>(gate_a + col)));
-                b = __fmul2_rn(b, __ldg(reinterpret_cast<const float2*>(gate_b + col)));
-            }
-            auto add = [](float2 v, Word w) {
-                if constexpr (F32) return __fadd2_rn(w, v);
-                else return __fadd2_rn(make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)), v);
-            };
-            auto put = [&](int64_t at, float2 v) {
-                if constexpr (F32) out[at + (col >> 1)] = v;
-                else out[at + (col >> 1)] = mx::bf16x2_bits(v.x, v.y);
-            };
-            if (on_a) put(ia, res ? add(a, wa[i]) : a);
-            if (on_b) put(ib, res ? add(b, wb[i]) : b);
-        }
-    }
-}
-
-// Bring a warp's part of the residual tile (32 rows x 128 columns) into L2
-// while its accumulator is still being computed.
-template <bool F32>
-__device__ __forceinline__ void prefetch_residual(const LinearParams& p, int64_t y0, int64_t x0, int lane) {
-    const int64_t row = y0 + lane;
-    if (!p.onto.r || row >= p.M || x0 >= p.N) return;
-    constexpr int W = F32 ? 4 : 2;
-    const char* at = static_cast<const char*>(p.onto.r) + (row * p.N + x0) * W;
-    const int bytes = static_cast<int>(min(static_cast<int64_t>(128), p.N - x0)) * W;
-    for (int o = 0; o < bytes; o += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + o));
+// As above, 64 columns (registers 4j .. 4j + 3 of eight blocks).
+__device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
 }
 
 template <bool F32>
@@ -249,9 +182,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PK_THREADS, 1)
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
     const uint32_t tmem = S.tmem_base;
-
-    if (warp == PK_PRODUCER) {
-        if (ptx::elect_one()) {
+    const int chunk = F32 ? FP32_CHUNK : p.ksteps;  // K-steps per accumulator
+    auto teardown = [&] {
+        __syncwarp();
+        ptx::tc_fence_before();
+        ptx::cluster_sync();
+        if (warp == 1) {
+            __syncwarp();
+            ptx::tc_fence_after();
+            ptx::tmem_dealloc_pair(tmem, 512);
+        }
+    };
+    // Each side of the register split ends with its own copy of the teardown.
+    if (warp >= PK_EPI_WARPS) {
+        ptx::setmaxnreg_dec<PK_CTRL_REGS>();
+        if (warp == PK_PRODUCER && ptx::elect_one()) {
             int stage = 0, last_stage = -1;
             uint32_t phase = 0, last_phase = 0;
             bool ok = true;
@@ -279,86 +224,121 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PK_THREADS, 1)
             if (last_stage >= 0 &&
                 !ptx::mbar_wait_bounded_cluster(ptx::smem_u32(&S.empty[last_stage]), last_phase, drain_ns, &never))
                 ptx::spin_ns(1000000);
-        }
-    } else if (warp == PK_MMA) {
-        if (leader && ptx::elect_one()) {
+        } else if (warp == PK_MMA && leader && ptx::elect_one()) {
             int stage = 0, it = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (int tile = pair; tile < tiles && ok; tile += npairs, ++it) {
-                const int buf = it & 1;
-                if (!ptx::mbar_wait_bounded_cluster(ptx::smem_u32(&S.acc_empty[buf]), ((it >> 1) & 1) ^ 1u,
-                                                    p.wait_limit_ns, abort)) {
-                    ok = false;
-                    break;
-                }
-                ptx::tc_fence_after();
-                const uint32_t acc = tmem + buf * PK_N;
-                for (int ks = 0; ks < p.ksteps; ++ks) {
-                    if (!ptx::mbar_wait_bounded(ptx::smem_u32(&S.full[stage]), phase, p.wait_limit_ns, abort)) {
+            for (int tile = pair; tile < tiles && ok; tile += npairs) {
+                for (int k0 = 0; k0 < p.ksteps && ok; k0 += chunk, ++it) {
+                    const int buf = it & 1, k1 = min(k0 + chunk, p.ksteps);
+                    if (!ptx::mbar_wait_bounded_cluster(ptx::smem_u32(&S.acc_empty[buf]), ((it >> 1) & 1) ^ 1u,
+                                                        p.wait_limit_ns, abort)) {
                         ok = false;
                         break;
                     }
                     ptx::tc_fence_after();
-                    const uint32_t a = ptx::smem_u32(S.a[stage]), b = ptx::smem_u32(S.b[stage]);
+                    const uint32_t acc = tmem + buf * PK_N;
+                    for (int ks = k0; ks < k1; ++ks) {
+                        if (!ptx::mbar_wait_bounded(ptx::smem_u32(&S.full[stage]), phase, p.wait_limit_ns, abort)) {
+                            ok = false;
+                            break;
+                        }
+                        ptx::tc_fence_after();
+                        const uint32_t a = ptx::smem_u32(S.a[stage]), b = ptx::smem_u32(S.b[stage]);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        ptx::mma_bf16_pair(acc, desc_sw128(a + kk * 32), desc_sw128(b + kk * 32), PK_IDESC,
-                                           (ks | kk) != 0);
-                    ptx::tc_commit_pair_mc(ptx::smem_u32(&S.empty[stage]), PAIR_MASK);
-                    if (++stage == PK_STAGES) { stage = 0; phase ^= 1u; }
+                        for (int kk = 0; kk < 4; ++kk)
+                            ptx::mma_bf16_pair(acc, desc_sw128(a + kk * 32), desc_sw128(b + kk * 32), PK_IDESC,
+                                               (ks != k0 || kk != 0) ? 1u : 0u);
+                        ptx::tc_commit_pair_mc(ptx::smem_u32(&S.empty[stage]), PAIR_MASK);
+                        if (++stage == PK_STAGES) { stage = 0; phase ^= 1u; }
+                    }
+                    if (!ok) break;
+                    ptx::tc_commit_pair_mc(ptx::smem_u32(&S.acc_full[buf]), PAIR_MASK);
                 }
-                if (!ok) break;
-                ptx::tc_commit_pair_mc(ptx::smem_u32(&S.acc_full[buf]), PAIR_MASK);
             }
             if (!ok) raise_abort(S, p.status);
             ptx::tc_commit_pair_mc(ptx::smem_u32(&S.drain), 0x1);
             ptx::mbar_wait_bounded(ptx::smem_u32(&S.drain), 0, drain_ns, &never);
         }
+        teardown();
     } else {
+        ptx::setmaxnreg_inc<PK_EPI_REGS>();
         const int q = warp & 3, half = warp >> 2;
-        const uint32_t empty_leader[2] = {ptx::mapa(ptx::smem_u32(&S.acc_empty[0]), 0),
-                                          ptx::mapa(ptx::smem_u32(&S.acc_empty[1]), 0)};
+        const uint32_t empty_leader = ptx::mapa(ptx::smem_u32(&S.acc_empty[0]), 0);
+        onto::Tile<F32> end;
         int it = 0;
-        for (int tile = pair; tile < tiles; tile += npairs, ++it) {
-            int m, n;
-            pair_coords(p, tile, m, n);
-            const int buf = it & 1;
-            const int64_t y0 = (int64_t)m * 256 + (int64_t)rank * ROWS + q * 32;
-            const int64_t x0 = (int64_t)n * PK_N + half * 128;
-            prefetch_residual<F32>(p, y0, x0, lane);
+        // the accumulator's chunk `it` is complete
+        auto wait_full = [&]() -> bool {
             int ok = 1;
             if (lane == 0)
-                ok = ptx::mbar_wait_bounded_long(ptx::smem_u32(&S.acc_full[buf]), (it >> 1) & 1, p.wait_limit_ns, abort,
+                ok = ptx::mbar_wait_bounded_long(ptx::smem_u32(&S.acc_full[it & 1]), (it >> 1) & 1, p.wait_limit_ns, abort,
                                                  20000u);
             ok = __shfl_sync(0xffffffffu, ok, 0);
-            if (!ok) {
-                if (lane == 0) raise_abort(S, p.status);
-                break;
-            }
+            if (!ok && lane == 0) raise_abort(S, p.status);
             ptx::tc_fence_after();
-            const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * PK_N + half * 128;
+            return ok;
+        };
+        // this warp has read it: the MMAs of the chunk after next may overwrite it
+        auto release = [&] {
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive_remote_relaxed(empty_leader + (it & 1) * 8);
+            ++it;
+        };
+        bool ok = true;
+        for (int tile = pair; tile < tiles && ok; tile += npairs) {
+            int m, n;
+            pair_coords(p, tile, m, n);
+            end.prepare(p.end, (int64_t)m * 256 + (int64_t)rank * ROWS + q * 32, (int64_t)n * PK_N + half * 128, lane,
+                        S.vectors[warp]);
+            if constexpr (F32) {
+                uint32_t sum[128];
 #pragma unroll 1
-            for (int sl = 0; sl < 2; ++sl) {
-                uint32_t r[64];
-                tmem_ld_16x256b_x16(taddr + (static_cast<uint32_t>(16 * sl) << 16), r);
-                ptx::tmem_ld_wait();
-                if (sl == 1) {  // drained: the MMAs of the tile after next may overwrite it
-                    ptx::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive_remote_relaxed(empty_leader[buf]);
+                for (int k0 = 0; k0 < p.ksteps; k0 += chunk) {
+                    if (!(ok = wait_full())) break;
+                    const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + (it & 1) * PK_N + half * 128;
+                    if (k0 == 0) {
+                        tmem_ld_16x256b_x16(taddr, sum);
+                        tmem_ld_16x256b_x16(taddr + (16u << 16), sum + 64);
+                        ptx::tmem_ld_wait();
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {  // slab i / 2, columns 64 (i % 2) ..
+                            uint32_t r[32];
+                            tmem_ld_16x256b_x8(taddr + (static_cast<uint32_t>(16 * (i >> 1)) << 16) + 64 * (i & 1), r);
+                            ptx::tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                sum[32 * i + e] = __float_as_uint(__fadd_rn(__uint_as_float(sum[32 * i + e]), __uint_as_float(r[e])));
+                        }
+                    }
+                    release();
                 }
-                if (x0 < p.N) pair_slab<F32>(p, y0 + 16 * sl, x0, lane, r);
+                if (!ok) break;
+                end.load_first(p.end, lane);
+                if (end.nj > 0) {
+#pragma unroll 1
+                    for (int sl = 0; sl < 2; ++sl) {
+                        end.template store<false, true>(p.end, sl, lane, S.vectors[warp], sum);
+#pragma unroll
+                        for (int e = 0; e < 64; ++e) sum[e] = sum[e + 64];
+                    }
+                }
+            } else {
+                end.load_first(p.end, lane);
+                if (!(ok = wait_full())) break;
+                const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + (it & 1) * PK_N + half * 128;
+#pragma unroll 1
+                for (int sl = 0; sl < 2; ++sl) {
+                    uint32_t r[64];
+                    tmem_ld_16x256b_x16(taddr + (static_cast<uint32_t>(16 * sl) << 16), r);
+                    ptx::tmem_ld_wait();
+                    if (sl == 1) release();
+                    if (end.nj > 0) end.template store<false, true>(p.end, sl, lane, S.vectors[warp], r);
+                }
             }
         }
-    }
-    __syncwarp();
-    ptx::tc_fence_before();
-    ptx::cluster_sync();
-    if (warp == 1) {
-        __syncwarp();
-        ptx::tc_fence_after();
-        ptx::tmem_dealloc_pair(tmem, 512);
+        teardown();
     }
 }
 
@@ -367,7 +347,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PK_THREADS, 1)
 constexpr int SK_THREADS = 192;  // warps 0-3 drain tensor memory, 4 issues the copies, 5 the MMAs
 
 // Ring slots: as many as leave room for two CTAs per SM (one for 256 tokens).
-__host__ __device__ constexpr int sk_stages(int nt) { return nt <= 32 ? 5 : (nt <= 64 ? 4 : (nt == 128 ? 3 : 4)); }
+__host__ __device__ constexpr int sk_stages(int nt) { return nt <= 32 ? 5 : (nt <= 64 ? 4 : 3); }
 
 template <int NT>
 struct __align__(1024) SkinnySmem {
@@ -381,6 +361,8 @@ struct __align__(1024) SkinnySmem {
     };
     uint64_t full[STAGES];
     uint64_t empty[STAGES];
+    uint64_t acc_full[2];   // FP32: a chunk's sum is complete
+    uint64_t acc_empty[2];  // FP32: the four draining warps have read it
     uint64_t done;
     uint32_t tmem_base;
     int abort_flag;
@@ -401,7 +383,9 @@ template <int NT, bool F32>
 __global__ void __launch_bounds__(SK_THREADS) skinny_kernel(const __grid_constant__ LinearParams p, int splits) {
     using SM = SkinnySmem<NT>;
     constexpr int STAGES = SM::STAGES;
-    constexpr uint32_t COLS = NT < 32 ? 32 : NT;
+    constexpr uint32_t ACC_COLS = NT < 32 ? 32 : NT;
+    constexpr uint32_t COLS = F32 ? 2 * ACC_COLS : ACC_COLS;
+    static_assert(!F32 || NT <= 64, "an FP32 lane holds the sums of all its tokens");
     extern __shared__ uint8_t smem_raw[];
     SM& S = *reinterpret_cast<SM*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -418,6 +402,10 @@ __global__ void __launch_bounds__(SK_THREADS) skinny_kernel(const __grid_constan
         for (int s = 0; s < STAGES; ++s) {
             ptx::mbar_init(ptx::smem_u32(&S.full[s]), 1);
             ptx::mbar_init(ptx::smem_u32(&S.empty[s]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(ptx::smem_u32(&S.acc_full[i]), 1);
+            ptx::mbar_init(ptx::smem_u32(&S.acc_empty[i]), 4);
         }
         ptx::mbar_init(ptx::smem_u32(&S.done), 1);
         S.abort_flag = 0;
@@ -468,6 +456,13 @@ __global__ void __launch_bounds__(SK_THREADS) skinny_kernel(const __grid_constan
             uint32_t phase = 0;
             bool ok = true;
             for (int ks = k0; ks < k1; ++ks) {
+                const int i = (ks - k0) / FP32_CHUNK, buf = F32 ? i & 1 : 0;
+                const bool first = F32 ? (ks - k0) % FP32_CHUNK == 0 : ks == k0;
+                if (F32 && first &&
+                    !ptx::mbar_wait_bounded(ptx::smem_u32(&S.acc_empty[buf]), ((i >> 1) & 1) ^ 1u, p.wait_limit_ns, abort)) {
+                    ok = false;
+                    break;
+                }
                 if (!ptx::mbar_wait_bounded(ptx::smem_u32(&S.full[stage]), phase, p.wait_limit_ns, abort)) {
                     ok = false;
                     break;
@@ -476,14 +471,48 @@ __global__ void __launch_bounds__(SK_THREADS) skinny_kernel(const __grid_constan
                 const uint32_t a = ptx::smem_u32(S.ring.w[stage]), b = ptx::smem_u32(S.ring.x[stage]);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    ptx::mma_bf16(tmem, desc_sw128(a + kk * 32), desc_sw128(b + kk * 32), idesc_bf16(ROWS, NT),
-                                  (ks != k0 || kk != 0) ? 1u : 0u);
+                    ptx::mma_bf16(tmem + buf * ACC_COLS, desc_sw128(a + kk * 32), desc_sw128(b + kk * 32),
+                                  idesc_bf16(ROWS, NT), (!first || kk != 0) ? 1u : 0u);
                 ptx::tc_commit(ptx::smem_u32(&S.empty[stage]));
+                if (F32 && (ks + 1 == k1 || (ks + 1 - k0) % FP32_CHUNK == 0)) ptx::tc_commit(ptx::smem_u32(&S.acc_full[buf]));
                 if (++stage == STAGES) { stage = 0; phase ^= 1u; }
             }
             if (!ok) raise_abort(S, p.status);
             ptx::tc_commit(ptx::smem_u32(&S.done));
             if (!ptx::mbar_wait_bounded(ptx::smem_u32(&S.done), 0, drain_ns, &never)) raise_abort(S, p.status);
+        }
+    }
+    // FP32: a lane adds up its channel's chunk sums for all tokens
+    float sum[F32 ? ACC_COLS : 1];
+    if constexpr (F32) {
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(ACC_COLS); ++i) sum[i] = 0.0f;
+        if (warp < 4) {
+            const int chunks = (k1 - k0 + FP32_CHUNK - 1) / FP32_CHUNK;
+#pragma unroll 1
+            for (int i = 0; i < chunks; ++i) {
+                int ok = 1;
+                if (lane == 0)
+                    ok = ptx::mbar_wait_bounded(ptx::smem_u32(&S.acc_full[i & 1]), (i >> 1) & 1, p.wait_limit_ns, abort);
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) {
+                    if (lane == 0) raise_abort(S, p.status);
+                    break;
+                }
+                ptx::tc_fence_after();
+                const uint32_t taddr = tmem + (static_cast<uint32_t>(warp * 32) << 16) + (i & 1) * ACC_COLS;
+#pragma unroll
+                for (int c = 0; c < static_cast<int>(ACC_COLS); c += 32) {
+                    uint32_t r[32];
+                    ptx::tmem_ld_32x32b_x32(taddr + c, r);
+                    ptx::tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) sum[c + e] = __fadd_rn(sum[c + e], __uint_as_float(r[e]));
+                }
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&S.acc_empty[i & 1]));
+            }
         }
     }
     // All copies have landed and all MMAs completed: the ring becomes the
@@ -492,7 +521,13 @@ __global__ void __launch_bounds__(SK_THREADS) skinny_kernel(const __grid_constan
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    if (warp < 4) {
+    if (F32) {
+        if (warp < 4) {
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+                if (m0 + i < p.end.M) S.part[i][warp * 32 + lane] = sum[F32 ? i : 0];
+        }
+    } else if (warp < 4) {
         const uint32_t taddr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
 #pragma unroll 1
         for (int c = 0; c < NT; c += 32) {
@@ -502,7 +537,7 @@ __global__ void __launch_bounds__(SK_THREADS) skinny_kernel(const __grid_constan
             const bool some = k1 > k0;  // a rank without K-steps adds zeros
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-                if (c + i < NT && m0 + c + i < p.M) S.part[c + i][warp * 32 + lane] = some ? __uint_as_float(r[i]) : 0.0f;
+                if (c + i < NT && m0 + c + i < p.end.M) S.part[c + i][warp * 32 + lane] = some ? __uint_as_float(r[i]) : 0.0f;
         }
         ptx::tc_fence_before();
     }
@@ -513,14 +548,14 @@ __global__ void __launch_bounds__(SK_THREADS) skinny_kernel(const __grid_constan
         ptx::tmem_dealloc(tmem, COLS);
     }
     // Each rank finishes its share of the tile: four channels of one token at a time.
-    const int mt = static_cast<int>(min(static_cast<int64_t>(NT), p.M - m0));
+    const int mt = static_cast<int>(min(static_cast<int64_t>(NT), p.end.M - m0));
     const int total = mt * (ROWS / 4), chunk = (total + splits - 1) / splits;
     const int end = min(total, (rank + 1) * chunk);
     const uint32_t part0 = ptx::smem_u32(&S.part[0][0]);
     for (int e = rank * chunk + static_cast<int>(threadIdx.x); e < end; e += SK_THREADS) {
         const int t = e / (ROWS / 4), c = (e % (ROWS / 4)) * 4;
         const int64_t n = n0 + c, m = m0 + t;
-        if (n >= p.N) continue;
+        if (n >= p.end.N) continue;
         const uint32_t off = part0 + (t * ROWS + c) * 4;
         float4 v;
         if (splits == 1) {
@@ -533,34 +568,34 @@ __global__ void __launch_bounds__(SK_THREADS) skinny_kernel(const __grid_constan
             }
         }
         float2 a = make_float2(v.x, v.y), b = make_float2(v.z, v.w);
-        if (p.bias) {
-            const float4 bb = __ldg(reinterpret_cast<const float4*>(p.bias + n));
+        if (p.end.bias) {
+            const float4 bb = __ldg(reinterpret_cast<const float4*>(p.end.bias + n));
             a = __fadd2_rn(a, make_float2(bb.x, bb.y));
             b = __fadd2_rn(b, make_float2(bb.z, bb.w));
         }
-        a = activate2(a, p.act);
-        b = activate2(b, p.act);
-        if (p.onto.gate) {
+        a = onto::activate2(a, p.end.act);
+        b = onto::activate2(b, p.end.act);
+        if (p.end.onto.gate) {
             const float4 g = __ldg(reinterpret_cast<const float4*>(
-                p.onto.gate + (static_cast<uint32_t>(m) / static_cast<uint32_t>(p.onto.gate_rows)) * p.onto.gate_stride + n));
+                p.end.onto.gate + (static_cast<uint32_t>(m) / static_cast<uint32_t>(p.end.onto.gate_rows)) * p.end.onto.gate_stride + n));
             a = __fmul2_rn(a, make_float2(g.x, g.y));
             b = __fmul2_rn(b, make_float2(g.z, g.w));
         }
-        const int64_t at = m * p.N + n;
+        const int64_t at = m * p.end.N + n;
         if constexpr (F32) {
-            if (p.onto.r) {
-                const float4 w = *reinterpret_cast<const float4*>(static_cast<const float*>(p.onto.r) + at);
+            if (p.end.onto.r) {
+                const float4 w = *reinterpret_cast<const float4*>(static_cast<const float*>(p.end.onto.r) + at);
                 a = __fadd2_rn(make_float2(w.x, w.y), a);
                 b = __fadd2_rn(make_float2(w.z, w.w), b);
             }
-            *reinterpret_cast<float4*>(static_cast<float*>(p.Y) + at) = make_float4(a.x, a.y, b.x, b.y);
+            *reinterpret_cast<float4*>(static_cast<float*>(p.end.Y) + at) = make_float4(a.x, a.y, b.x, b.y);
         } else {
-            if (p.onto.r) {
-                const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.onto.r) + at);
+            if (p.end.onto.r) {
+                const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.end.onto.r) + at);
                 a = __fadd2_rn(make_float2(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u)), a);
                 b = __fadd2_rn(make_float2(__uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u)), b);
             }
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.Y) + at) =
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.end.Y) + at) =
                 make_uint2(mx::bf16x2_bits(a.x, a.y), mx::bf16x2_bits(b.x, b.y));
         }
     }
@@ -596,6 +631,12 @@ int launch_pair(LinearParams& p, bool f32, int64_t w_bytes, cudaStream_t st) {
     {
         std::lock_guard<std::mutex> lk(mu);
         if (!ki.ready) {
+            // the register split assumes that the launch gives every thread exactly PK_LAUNCH_REGS
+            cudaFuncAttributes fa;
+            OSM_TRY(check_cuda(cudaFuncGetAttributes(&fa, kern), "linear_hp attributes"));
+            if (fa.numRegs != PK_LAUNCH_REGS)
+                return fail(OSM_ERR_UNSUPPORTED, "linear_hp: built with %d registers per thread, the split needs %d",
+                            fa.numRegs, PK_LAUNCH_REGS);
             OSM_TRY(check_cuda(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                     static_cast<int>(smem)), "linear_hp smem attribute"));
             cudaLaunchConfig_t cfg = {};
@@ -614,8 +655,8 @@ int launch_pair(LinearParams& p, bool f32, int64_t w_bytes, cudaStream_t st) {
             ki.ready = true;
         }
     }
-    p.num_m = static_cast<int>(ceil_div(p.M, 256));
-    p.num_n = static_cast<int>(ceil_div(p.N, PK_N));
+    p.num_m = static_cast<int>(ceil_div(p.end.M, 256));
+    p.num_n = static_cast<int>(ceil_div(p.end.N, PK_N));
     p.group_m = w_bytes <= W_RESIDENT_BYTES ? 1 : 8;
     const int64_t tiles = static_cast<int64_t>(p.num_m) * p.num_n;
     if (tiles > 0x7FFFFFFF) return fail(OSM_ERR_UNSUPPORTED, "linear_hp: too many tiles");
@@ -632,16 +673,16 @@ int launch_pair(LinearParams& p, bool f32, int64_t w_bytes, cudaStream_t st) {
     return check_cuda(cudaLaunchKernelEx(&cfg, kern, p), "linear_hp launch");
 }
 
-template <int NT>
-int launch_skinny(LinearParams& p, bool f32, int splits, cudaStream_t st) {
-    void (*kern)(LinearParams, int) = f32 ? skinny_kernel<NT, true> : skinny_kernel<NT, false>;
+template <int NT, bool F32>
+int launch_skinny(LinearParams& p, int splits, cudaStream_t st) {
+    void (*kern)(LinearParams, int) = skinny_kernel<NT, F32>;
     constexpr size_t smem = sizeof(SkinnySmem<NT>) + 1024;
     static_assert(smem <= 232448, "shared memory budget");
-    static KernelInfo info[64][2];
+    static KernelInfo info[64];
     static std::mutex mu;
     int dev = 0;
     OSM_TRY(current_device(&dev));
-    KernelInfo& ki = info[dev][f32 ? 1 : 0];
+    KernelInfo& ki = info[dev];
     {
         std::lock_guard<std::mutex> lk(mu);
         if (!ki.ready) {
@@ -650,10 +691,10 @@ int launch_skinny(LinearParams& p, bool f32, int splits, cudaStream_t st) {
             ki.ready = true;
         }
     }
-    const int64_t mtiles = ceil_div(p.M, NT);
+    const int64_t mtiles = ceil_div(p.end.M, NT);
     if (mtiles > 65535) return fail(OSM_ERR_UNSUPPORTED, "linear_hp: too many token tiles");
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(p.N, ROWS) * splits), static_cast<unsigned>(mtiles), 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(p.end.N, ROWS) * splits), static_cast<unsigned>(mtiles), 1);
     cfg.blockDim = dim3(SK_THREADS, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
@@ -675,22 +716,17 @@ int launch_linear_hp(const osm_plan* pl, const uint16_t* X, int64_t M, const uin
                      const Onto& onto, void* Y, int y_dtype, cudaStream_t st) {
     LinearParams p;
     std::memset(&p, 0, sizeof(p));
-    p.bias = bias;
-    p.Y = Y;
-    p.onto = onto;
+    p.end = onto::Params{M, pl->N, bias, Y, onto, 1.0f, act};
     p.status = pl->d_status;
     p.wait_limit_ns = pl->wait_limit_ns;
-    p.M = M;
-    p.N = pl->N;
     p.ksteps = static_cast<int>(pl->kp / KSTEP);
-    p.act = act;
     const bool f32 = y_dtype == OSM_DT_F32;
     const int64_t ntiles = ceil_div(pl->N, ROWS);
     // Tokens per tile: the smallest width that takes them all, up to 256; from
     // there on CTA pairs, once their tiles fill the GPU.
     const int64_t pair_tiles = ceil_div(M, 256) * ceil_div(pl->N, PK_N);
     const bool pair = M > 256 && pair_tiles >= 74;
-    int nt = M <= 16 ? 16 : (M <= 32 ? 32 : (M <= 64 ? 64 : 128));
+    int nt = M <= 16 ? 16 : (M <= 32 ? 32 : (M <= 64 || f32 ? 64 : 128));
     // K is split until the CTAs cover the SMs, each rank keeping four K-steps or more.
     int splits = 1;
     const int64_t ctas = ntiles * ceil_div(M, nt);
@@ -700,10 +736,15 @@ int launch_linear_hp(const osm_plan* pl, const uint16_t* X, int64_t M, const uin
     OSM_TRY(make_map(&p.tm_x, bf, X, pl->K, M, pl->K * 2, KSTEP, pair ? ROWS : nt, sw, "X"));
     OSM_TRY(make_map(&p.tm_w, bf, w_hp, pl->kp, pl->N, pl->kp * 2, KSTEP, ROWS, sw, "w_hp"));
     if (pair) return launch_pair(p, f32, pl->N * pl->kp * 2, st);
-    if (nt == 16) return launch_skinny<16>(p, f32, splits, st);
-    if (nt == 32) return launch_skinny<32>(p, f32, splits, st);
-    if (nt == 64) return launch_skinny<64>(p, f32, splits, st);
-    return launch_skinny<128>(p, f32, splits, st);
+    if (f32) {
+        if (nt == 16) return launch_skinny<16, true>(p, splits, st);
+        if (nt == 32) return launch_skinny<32, true>(p, splits, st);
+        return launch_skinny<64, true>(p, splits, st);
+    }
+    if (nt == 16) return launch_skinny<16, false>(p, splits, st);
+    if (nt == 32) return launch_skinny<32, false>(p, splits, st);
+    if (nt == 64) return launch_skinny<64, false>(p, splits, st);
+    return launch_skinny<128, false>(p, splits, st);
 }
 
 }  // namespace osm

@@ -1,0 +1,167 @@
+// The end of a product in tensor memory: scaled, biased, activated, gated,
+// added to the residual stream and rounded once, for the GEMM kernels whose
+// epilogue warps hold 32 rows x 128 columns of a tile as two slabs of 16 rows
+// (tcgen05.ld 16x256b: thread t has rows t / 4 and t / 4 + 8 and, of each
+// 8-column block j, columns 2 (t % 4) and the next in registers 4j .. 4j + 3).
+//
+// Nothing of the store loop waits on global memory: the residual words of a
+// slab are in registers before its accumulator (those of a tile's first slab
+// are loaded while the MMAs still run, those of the second as the first one's
+// are used up), bias and gate are in shared memory. Loaded in the store loop
+// instead they doubled dual_gemm's time at 4096 x 5120 x 5120 (104 -> 201 us).
+#pragma once
+
+#include <cstdint>
+#include <type_traits>
+
+#include "osm_internal.h"
+#include "osm_mx.cuh"
+
+namespace osm {
+namespace onto {
+
+struct Params {
+    int64_t M, N;
+    const float* bias;   // [N] or NULL
+    void* Y;             // [M][N]; may be onto.r: a thread reads each word of r before it writes that word of Y
+    Onto onto;
+    float scale;         // of the accumulator (used by SCALED kernels)
+    int act;             // OSM_ACT_* (used by ACT kernels)
+};
+
+// x / (1 + 2^z) with z = -x log2(e); z is capped so that 1 + 2^z stays finite.
+__device__ __forceinline__ float2 silu2(float2 x) {
+    const float2 z = __fmul2_rn(x, make_float2(-1.44269504f, -1.44269504f));
+    const float2 d = __fadd2_rn(make_float2(mx::ex2_approx(fminf(z.x, 126.0f)), mx::ex2_approx(fminf(z.y, 126.0f))),
+                                make_float2(1.0f, 1.0f));
+    return __fmul2_rn(x, make_float2(mx::rcp_approx(d.x), mx::rcp_approx(d.y)));
+}
+__device__ __forceinline__ float2 activate2(float2 v, int act) {
+    if (act == OSM_ACT_GELU) return mx::gelu2(v);
+    if (act == OSM_ACT_SILU) return silu2(v);
+    return v;
+}
+
+template <bool F32>
+using Word = typename std::conditional<F32, float2, uint32_t>::type;  // two values of the stream
+
+template <bool F32>
+__device__ __forceinline__ Word<F32> to_word(float2 v) {
+    if constexpr (F32) return v;
+    else return mx::bf16x2_bits(v.x, v.y);
+}
+template <bool F32>
+__device__ __forceinline__ float2 from_word(Word<F32> w) {
+    if constexpr (F32) return w;
+    else return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+// Bias and gate of a warp's 128 columns, when all its rows share a gate row.
+struct Vectors {
+    float4 bias[32], gate[32];
+};
+
+// One warp's part of a tile: rows y0 .. y0 + 31, columns x0 .. x0 + 127.
+template <bool F32>
+struct Tile {
+    int64_t y0, x0;
+    int nj;              // 8-column blocks that exist (N % 32 == 0)
+    bool staged;         // gate (if any) is in Vectors
+    Word<F32> w[32];     // residual words of the slab at hand
+
+    __device__ __forceinline__ static Word<F32>* at(const void* base, const Params& p, int64_t row, int64_t col) {
+        return static_cast<Word<F32>*>(const_cast<void*>(base)) + row * (p.N >> 1) + (col >> 1);
+    }
+    // To be called before the wait for the accumulator.
+    __device__ __forceinline__ void prepare(const Params& p, int64_t row0, int64_t col0, int lane, Vectors& v) {
+        y0 = row0;
+        x0 = col0;
+        nj = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(16), (p.N - x0) >> 3)));
+        staged = true;
+        if (y0 >= p.M || nj == 0) return;
+        uint32_t group = 0;
+        if (p.onto.gate) {
+            const uint32_t share = static_cast<uint32_t>(p.onto.gate_rows);
+            group = static_cast<uint32_t>(y0) / share;
+            staged = static_cast<uint32_t>(min(y0 + 31, p.M - 1)) / share == group;
+        }
+        __syncwarp();  // the last tile's readers are done
+        const int64_t c = x0 + 4 * lane;
+        if (c < p.N) {
+            if (p.bias) v.bias[lane] = __ldg(reinterpret_cast<const float4*>(p.bias + c));
+            if (p.onto.gate && staged)
+                v.gate[lane] = __ldg(reinterpret_cast<const float4*>(p.onto.gate + group * p.onto.gate_stride + c));
+        }
+        __syncwarp();
+        // the residual words are read later: bring them into L2
+        const int64_t row = y0 + lane;
+        if (p.onto.r && row < p.M) {
+            const char* from = reinterpret_cast<const char*>(at(p.onto.r, p, row, x0));
+            for (int o = 0; o < nj * 8 * (F32 ? 4 : 2); o += 128)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(from + o));
+        }
+    }
+    // The first slab's residual words; before the wait for the accumulator
+    // where the registers allow.
+    __device__ __forceinline__ void load_first(const Params& p, int lane) {
+        if (!p.onto.r) return;
+        const int64_t ra = y0 + (lane >> 2), rb = ra + 8, col = x0 + 2 * (lane & 3);
+        const Word<F32> *pa = at(p.onto.r, p, ra, col), *pb = at(p.onto.r, p, rb, col);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            if (j < nj && ra < p.M) w[2 * j] = pa[4 * j];
+            if (j < nj && rb < p.M) w[2 * j + 1] = pb[4 * j];
+        }
+    }
+    // Slab sl (0, 1) from its 64 accumulator registers.
+    template <bool SCALED, bool ACT>
+    __device__ __forceinline__ void store(const Params& p, int sl, int lane, const Vectors& v, const uint32_t* r) {
+        const int64_t ra = y0 + 16 * sl + (lane >> 2), rb = ra + 8, c0 = x0 + 2 * (lane & 3);
+        const bool on_a = ra < p.M, on_b = rb < p.M, more = p.onto.r != nullptr && sl == 0;
+        const bool next_a = more && ra + 16 < p.M, next_b = more && rb + 16 < p.M;
+        const float *gate_a = nullptr, *gate_b = nullptr;
+        if (!staged) {  // rows past M read the last row's gate
+            const uint32_t last = static_cast<uint32_t>(p.M - 1), share = static_cast<uint32_t>(p.onto.gate_rows);
+            gate_a = p.onto.gate + (min(static_cast<uint32_t>(ra), last) / share) * p.onto.gate_stride + c0;
+            gate_b = p.onto.gate + (min(static_cast<uint32_t>(rb), last) / share) * p.onto.gate_stride + c0;
+        }
+        const Word<F32>* na = at(p.onto.r, p, ra + 16, c0);
+        const int64_t step = 4 * p.N;  // words between rows 8 apart
+        Word<F32>* oa = at(p.Y, p, ra, c0);
+        const float2* vb = reinterpret_cast<const float2*>(v.bias) + (lane & 3);
+        const float2* vg = reinterpret_cast<const float2*>(v.gate) + (lane & 3);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            if (j >= nj) break;
+            float2 a = make_float2(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]));
+            float2 b = make_float2(__uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
+            if constexpr (SCALED) {
+                a = __fmul2_rn(a, make_float2(p.scale, p.scale));
+                b = __fmul2_rn(b, make_float2(p.scale, p.scale));
+            }
+            if (p.bias) {
+                a = __fadd2_rn(a, vb[4 * j]);
+                b = __fadd2_rn(b, vb[4 * j]);
+            }
+            if constexpr (ACT) {
+                a = activate2(a, p.act);
+                b = activate2(b, p.act);
+            }
+            if (p.onto.gate) {
+                a = __fmul2_rn(a, staged ? vg[4 * j] : __ldg(reinterpret_cast<const float2*>(gate_a + 8 * j)));
+                b = __fmul2_rn(b, staged ? vg[4 * j] : __ldg(reinterpret_cast<const float2*>(gate_b + 8 * j)));
+            }
+            if (p.onto.r) {
+                a = __fadd2_rn(from_word<F32>(w[2 * j]), a);
+                b = __fadd2_rn(from_word<F32>(w[2 * j + 1]), b);
+                if (next_a) w[2 * j] = na[4 * j];
+                if (next_b) w[2 * j + 1] = na[step + 4 * j];
+            }
+            if (on_a) oa[4 * j] = to_word<F32>(a);
+            if (on_b) oa[step + 4 * j] = to_word<F32>(b);
+        }
+    }
+};
+
+}  // namespace onto
+}  // namespace osm
