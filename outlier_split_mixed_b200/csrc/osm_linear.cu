@@ -7,7 +7,7 @@
 //                 of a tile runs under the MMAs of the next.
 //   skinny_kernel few tokens: the weights are what has to be read. The
 //                 operands change places -- 128 output channels are the rows
-//                 of the MMA, NT tokens its columns -- and the CTAs of a
+//                 of the MMA, nt tokens its columns -- and the CTAs of a
 //                 cluster split K, so that every SM streams weights; the
 //                 partial sums are joined through distributed shared memory
 //                 in the order of the ranks.
@@ -20,9 +20,11 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 
 #include "osm_internal.h"
 #include "osm_mx.cuh"
@@ -346,21 +348,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PK_THREADS, 1)
 
 constexpr int SK_THREADS = 192;  // warps 0-3 drain tensor memory, 4 issues the copies, 5 the MMAs
 
-// Ring slots: as many as leave room for two CTAs per SM (one for 256 tokens).
-__host__ __device__ constexpr int sk_stages(int nt) { return nt <= 32 ? 5 : (nt <= 64 ? 4 : 3); }
+constexpr int SK_MAX_STAGES = 8;
 
-template <int NT>
-struct __align__(1024) SkinnySmem {
-    static constexpr int STAGES = sk_stages(NT);
-    union {
-        struct {
-            uint8_t w[STAGES][TILE];
-            uint8_t x[STAGES][NT * 128];
-        } ring;
-        float part[NT][ROWS];  // the CTA's partial sums, token-major, once the ring is idle
-    };
-    uint64_t full[STAGES];
-    uint64_t empty[STAGES];
+// Bytes of a ring slot: 128 weight rows and nt token rows of one K-step.
+__host__ __device__ constexpr int sk_slot(int nt) { return TILE + nt * 128; }
+
+struct SkinnyControl {
+    uint64_t full[SK_MAX_STAGES];
+    uint64_t empty[SK_MAX_STAGES];
     uint64_t acc_full[2];   // FP32: a chunk's sum is complete
     uint64_t acc_empty[2];  // FP32: the four draining warps have read it
     uint64_t done;
@@ -377,21 +372,26 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
     return v;
 }
 
-// Grid: x = clusters of S CTAs over the 128-channel tiles, y = token tiles.
-// Rank s of a cluster takes the K-steps [s ks / S, (s + 1) ks / S).
-template <int NT, bool F32>
-__global__ void __launch_bounds__(SK_THREADS) skinny_kernel(const __grid_constant__ LinearParams p, int splits) {
-    using SM = SkinnySmem<NT>;
-    constexpr int STAGES = SM::STAGES;
-    constexpr uint32_t ACC_COLS = NT < 32 ? 32 : NT;
-    constexpr uint32_t COLS = F32 ? 2 * ACC_COLS : ACC_COLS;
-    static_assert(!F32 || NT <= 64, "an FP32 lane holds the sums of all its tokens");
+// Grid: x = clusters of S CTAs over the 128-channel tiles, y = tiles of nt
+// tokens (a multiple of 16, at most 256). Rank s of a cluster takes the K-steps
+// [s ks / S, (s + 1) ks / S). Once its ring is idle it holds the CTA's partial
+// sums [nt][128]. SUMS: 0 for a BF16 result; for an FP32 one the tokens whose
+// sums a lane holds (nt <= SUMS).
+template <int SUMS>
+__global__ void __launch_bounds__(SK_THREADS) skinny_kernel(const __grid_constant__ LinearParams p, int splits, int nt,
+                                                           int stages, uint32_t acc_cols) {
+    constexpr bool F32 = SUMS > 0;
+    using Quad = typename std::conditional<F32, float4, uint2>::type;  // four values of Y's type
+    const uint32_t cols = F32 ? 2 * acc_cols : acc_cols;  // tensor-memory columns: a power of two, 32 or more
     extern __shared__ uint8_t smem_raw[];
-    SM& S = *reinterpret_cast<SM*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ SkinnyControl S;
+    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float* part = reinterpret_cast<float*>(ring);
+    const uint32_t ring_u32 = ptx::smem_u32(ring), slot_bytes = sk_slot(nt);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = splits > 1 ? static_cast<int>(ptx::cluster_ctarank()) : 0;
     const int n0 = (static_cast<int>(blockIdx.x) / splits) * ROWS;
-    const int m0 = static_cast<int>(blockIdx.y) * NT;
+    const int m0 = static_cast<int>(blockIdx.y) * nt;
     const int k0 = static_cast<int>(static_cast<int64_t>(p.ksteps) * rank / splits);
     const int k1 = static_cast<int>(static_cast<int64_t>(p.ksteps) * (rank + 1) / splits);
     const volatile int* abort = &S.abort_flag;
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(SK_THREADS) skinny_kernel(const __grid_constan
     const uint64_t drain_ns = p.wait_limit_ns > 200000000ull ? p.wait_limit_ns : 200000000ull;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) {
+        for (int s = 0; s < stages; ++s) {
             ptx::mbar_init(ptx::smem_u32(&S.full[s]), 1);
             ptx::mbar_init(ptx::smem_u32(&S.empty[s]), 1);
         }
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(SK_THREADS) skinny_kernel(const __grid_constan
         ptx::prefetch_tmap(&p.tm_w);
     }
     if (warp == 1) {
-        ptx::tmem_alloc(ptx::smem_u32(&S.tmem_base), COLS);
+        ptx::tmem_alloc(ptx::smem_u32(&S.tmem_base), cols);
         ptx::tmem_relinquish();
     }
     ptx::tc_fence_before();
@@ -438,20 +438,21 @@ __global__ void __launch_bounds__(SK_THREADS) skinny_kernel(const __grid_constan
                     break;
                 }
                 const uint32_t fb = ptx::smem_u32(&S.full[stage]);
-                ptx::mbar_arrive_expect_tx(fb, TILE + NT * 128);
-                ptx::tma_load_2d(ptx::smem_u32(S.ring.w[stage]), &p.tm_w, ks * KSTEP, n0, fb);
-                ptx::tma_load_2d(ptx::smem_u32(S.ring.x[stage]), &p.tm_x, ks * KSTEP, m0, fb);
-                if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                ptx::mbar_arrive_expect_tx(fb, slot_bytes);
+                ptx::tma_load_2d(ring_u32 + stage * slot_bytes, &p.tm_w, ks * KSTEP, n0, fb);
+                ptx::tma_load_2d(ring_u32 + stage * slot_bytes + TILE, &p.tm_x, ks * KSTEP, m0, fb);
+                if (++stage == stages) { stage = 0; phase ^= 1u; }
             }
             if (!ok) raise_abort(S, p.status);
             // every copy has landed before the ring is used again (the MMAs wait for each of them;
             // an aborted pipeline may not have)
-            for (int i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
-                if (!ptx::mbar_wait_bounded(ptx::smem_u32(&S.full[i % STAGES]), (i / STAGES) & 1, drain_ns, &never))
+            for (int i = issued > stages ? issued - stages : 0; i < issued; ++i)
+                if (!ptx::mbar_wait_bounded(ptx::smem_u32(&S.full[i % stages]), (i / stages) & 1, drain_ns, &never))
                     ptx::spin_ns(1000000);
         }
     } else if (warp == 5) {
         if (ptx::elect_one()) {
+            const uint32_t idesc = idesc_bf16(ROWS, nt);
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
@@ -468,25 +469,27 @@ __global__ void __launch_bounds__(SK_THREADS) skinny_kernel(const __grid_constan
                     break;
                 }
                 ptx::tc_fence_after();
-                const uint32_t a = ptx::smem_u32(S.ring.w[stage]), b = ptx::smem_u32(S.ring.x[stage]);
+                const uint32_t a = ring_u32 + stage * slot_bytes, b = a + TILE;
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    ptx::mma_bf16(tmem + buf * ACC_COLS, desc_sw128(a + kk * 32), desc_sw128(b + kk * 32),
-                                  idesc_bf16(ROWS, NT), (!first || kk != 0) ? 1u : 0u);
+                    ptx::mma_bf16(tmem + buf * acc_cols, desc_sw128(a + kk * 32), desc_sw128(b + kk * 32),
+                                  idesc, (!first || kk != 0) ? 1u : 0u);
                 ptx::tc_commit(ptx::smem_u32(&S.empty[stage]));
                 if (F32 && (ks + 1 == k1 || (ks + 1 - k0) % FP32_CHUNK == 0)) ptx::tc_commit(ptx::smem_u32(&S.acc_full[buf]));
-                if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                if (++stage == stages) { stage = 0; phase ^= 1u; }
             }
             if (!ok) raise_abort(S, p.status);
             ptx::tc_commit(ptx::smem_u32(&S.done));
             if (!ptx::mbar_wait_bounded(ptx::smem_u32(&S.done), 0, drain_ns, &never)) raise_abort(S, p.status);
         }
     }
+    float4 bias = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // of the channels that this lane finishes
+    if (p.end.bias && n0 + 4 * lane < p.end.N) bias = __ldg(reinterpret_cast<const float4*>(p.end.bias + n0 + 4 * lane));
     // FP32: a lane adds up its channel's chunk sums for all tokens
-    float sum[F32 ? ACC_COLS : 1];
+    float sum[F32 ? SUMS : 1];
     if constexpr (F32) {
 #pragma unroll
-        for (int i = 0; i < static_cast<int>(ACC_COLS); ++i) sum[i] = 0.0f;
+        for (int i = 0; i < SUMS; ++i) sum[i] = 0.0f;
         if (warp < 4) {
             const int chunks = (k1 - k0 + FP32_CHUNK - 1) / FP32_CHUNK;
 #pragma unroll 1
@@ -500,9 +503,10 @@ __global__ void __launch_bounds__(SK_THREADS) skinny_kernel(const __grid_constan
                     break;
                 }
                 ptx::tc_fence_after();
-                const uint32_t taddr = tmem + (static_cast<uint32_t>(warp * 32) << 16) + (i & 1) * ACC_COLS;
+                const uint32_t taddr = tmem + (static_cast<uint32_t>(warp * 32) << 16) + (i & 1) * acc_cols;
 #pragma unroll
-                for (int c = 0; c < static_cast<int>(ACC_COLS); c += 32) {
+                for (int c = 0; c < SUMS; c += 32) {
+                    if (c >= static_cast<int>(acc_cols)) break;
                     uint32_t r[32];
                     ptx::tmem_ld_32x32b_x32(taddr + c, r);
                     ptx::tmem_ld_wait();
@@ -524,20 +528,20 @@ __global__ void __launch_bounds__(SK_THREADS) skinny_kernel(const __grid_constan
     if (F32) {
         if (warp < 4) {
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
-                if (m0 + i < p.end.M) S.part[i][warp * 32 + lane] = sum[F32 ? i : 0];
+            for (int i = 0; i < SUMS; ++i)
+                if (i < nt && m0 + i < p.end.M) part[i * ROWS + warp * 32 + lane] = sum[F32 ? i : 0];
         }
     } else if (warp < 4) {
         const uint32_t taddr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
 #pragma unroll 1
-        for (int c = 0; c < NT; c += 32) {
+        for (int c = 0; c < nt; c += 32) {
             uint32_t r[32];
             ptx::tmem_ld_32x32b_x32(taddr + c, r);
             ptx::tmem_ld_wait();
             const bool some = k1 > k0;  // a rank without K-steps adds zeros
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-                if (c + i < NT && m0 + c + i < p.end.M) S.part[c + i][warp * 32 + lane] = some ? __uint_as_float(r[i]) : 0.0f;
+                if (c + i < nt && m0 + c + i < p.end.M) part[(c + i) * ROWS + warp * 32 + lane] = some ? __uint_as_float(r[i]) : 0.0f;
         }
         ptx::tc_fence_before();
     }
@@ -545,58 +549,71 @@ __global__ void __launch_bounds__(SK_THREADS) skinny_kernel(const __grid_constan
     else __syncthreads();
     if (warp == 1) {
         ptx::tc_fence_after();
-        ptx::tmem_dealloc(tmem, COLS);
+        ptx::tmem_dealloc(tmem, cols);
     }
-    // Each rank finishes its share of the tile: four channels of one token at a time.
-    const int mt = static_cast<int>(min(static_cast<int64_t>(NT), p.end.M - m0));
-    const int total = mt * (ROWS / 4), chunk = (total + splits - 1) / splits;
-    const int end = min(total, (rank + 1) * chunk);
-    const uint32_t part0 = ptx::smem_u32(&S.part[0][0]);
-    for (int e = rank * chunk + static_cast<int>(threadIdx.x); e < end; e += SK_THREADS) {
-        const int t = e / (ROWS / 4), c = (e % (ROWS / 4)) * 4;
-        const int64_t n = n0 + c, m = m0 + t;
-        if (n >= p.end.N) continue;
-        const uint32_t off = part0 + (t * ROWS + c) * 4;
-        float4 v;
-        if (splits == 1) {
-            v = *reinterpret_cast<const float4*>(&S.part[t][c]);
-        } else {
-            v = ld_cluster_f4(ptx::mapa(off, 0));
+    // Each rank finishes its share of the tile's tokens, a warp a token at a
+    // time, a lane four channels of it. Everything that UNROLL tokens read is
+    // on its way before the first of them is used.
+    constexpr int UNROLL = 4, WARPS = SK_THREADS / 32;
+    const int mt = static_cast<int>(min(static_cast<int64_t>(nt), p.end.M - m0)), share = (mt + splits - 1) / splits;
+    const int last = min(mt, (rank + 1) * share);
+    const int64_t n = n0 + 4 * lane;
+    if (n < p.end.N) {
+        for (int t0 = rank * share + warp; t0 < last; t0 += UNROLL * WARPS) {
+            float4 v[UNROLL], g[UNROLL];
+            Quad w[UNROLL];
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u) {
+                const int t = t0 + u * WARPS;
+                if (t >= last) break;
+                const uint32_t off = ring_u32 + (t * ROWS + 4 * lane) * 4;
+                v[u] = splits == 1 ? *reinterpret_cast<const float4*>(part + t * ROWS + 4 * lane) : ld_cluster_f4(ptx::mapa(off, 0));
+                if (p.end.onto.gate)
+                    g[u] = __ldg(reinterpret_cast<const float4*>(
+                        p.end.onto.gate +
+                        (static_cast<uint32_t>(m0 + t) / static_cast<uint32_t>(p.end.onto.gate_rows)) * p.end.onto.gate_stride + n));
+                if (p.end.onto.r) w[u] = static_cast<const Quad*>(p.end.onto.r)[((m0 + t) * p.end.N + n) >> 2];
+            }
             for (int s = 1; s < splits; ++s) {
-                const float4 o = ld_cluster_f4(ptx::mapa(off, s));
-                v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+#pragma unroll
+                for (int u = 0; u < UNROLL; ++u) {
+                    const int t = t0 + u * WARPS;
+                    if (t >= last) break;
+                    const float4 o = ld_cluster_f4(ptx::mapa(ring_u32 + (t * ROWS + 4 * lane) * 4, s));
+                    v[u] = make_float4(v[u].x + o.x, v[u].y + o.y, v[u].z + o.z, v[u].w + o.w);
+                }
             }
-        }
-        float2 a = make_float2(v.x, v.y), b = make_float2(v.z, v.w);
-        if (p.end.bias) {
-            const float4 bb = __ldg(reinterpret_cast<const float4*>(p.end.bias + n));
-            a = __fadd2_rn(a, make_float2(bb.x, bb.y));
-            b = __fadd2_rn(b, make_float2(bb.z, bb.w));
-        }
-        a = onto::activate2(a, p.end.act);
-        b = onto::activate2(b, p.end.act);
-        if (p.end.onto.gate) {
-            const float4 g = __ldg(reinterpret_cast<const float4*>(
-                p.end.onto.gate + (static_cast<uint32_t>(m) / static_cast<uint32_t>(p.end.onto.gate_rows)) * p.end.onto.gate_stride + n));
-            a = __fmul2_rn(a, make_float2(g.x, g.y));
-            b = __fmul2_rn(b, make_float2(g.z, g.w));
-        }
-        const int64_t at = m * p.end.N + n;
-        if constexpr (F32) {
-            if (p.end.onto.r) {
-                const float4 w = *reinterpret_cast<const float4*>(static_cast<const float*>(p.end.onto.r) + at);
-                a = __fadd2_rn(make_float2(w.x, w.y), a);
-                b = __fadd2_rn(make_float2(w.z, w.w), b);
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u) {
+                const int t = t0 + u * WARPS;
+                if (t >= last) break;
+                float2 a = make_float2(v[u].x, v[u].y), b = make_float2(v[u].z, v[u].w);
+                if (p.end.bias) {
+                    a = __fadd2_rn(a, make_float2(bias.x, bias.y));
+                    b = __fadd2_rn(b, make_float2(bias.z, bias.w));
+                }
+                a = onto::activate2(a, p.end.act);
+                b = onto::activate2(b, p.end.act);
+                if (p.end.onto.gate) {
+                    a = __fmul2_rn(a, make_float2(g[u].x, g[u].y));
+                    b = __fmul2_rn(b, make_float2(g[u].z, g[u].w));
+                }
+                Quad out;
+                if constexpr (F32) {
+                    if (p.end.onto.r) {
+                        a = __fadd2_rn(make_float2(w[u].x, w[u].y), a);
+                        b = __fadd2_rn(make_float2(w[u].z, w[u].w), b);
+                    }
+                    out = make_float4(a.x, a.y, b.x, b.y);
+                } else {
+                    if (p.end.onto.r) {
+                        a = __fadd2_rn(onto::from_word<false>(w[u].x), a);
+                        b = __fadd2_rn(onto::from_word<false>(w[u].y), b);
+                    }
+                    out = make_uint2(mx::bf16x2_bits(a.x, a.y), mx::bf16x2_bits(b.x, b.y));
+                }
+                static_cast<Quad*>(p.end.Y)[((m0 + t) * p.end.N + n) >> 2] = out;
             }
-            *reinterpret_cast<float4*>(static_cast<float*>(p.end.Y) + at) = make_float4(a.x, a.y, b.x, b.y);
-        } else {
-            if (p.end.onto.r) {
-                const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.end.onto.r) + at);
-                a = __fadd2_rn(make_float2(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u)), a);
-                b = __fadd2_rn(make_float2(__uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u)), b);
-            }
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.end.Y) + at) =
-                make_uint2(mx::bf16x2_bits(a.x, a.y), mx::bf16x2_bits(b.x, b.y));
         }
     }
     // a CTA's partial sums stay until every rank has read them
@@ -606,7 +623,7 @@ __global__ void __launch_bounds__(SK_THREADS) skinny_kernel(const __grid_constan
 // ------------------------------------------------------------ host
 
 struct KernelInfo {
-    int clusters = 0;  // co-resident CTA pairs (pair_kernel); 1 once prepared (skinny_kernel)
+    int clusters = 0;  // co-resident CTA pairs (pair_kernel)
     bool ready = false;
 };
 
@@ -673,28 +690,74 @@ int launch_pair(LinearParams& p, bool f32, int64_t w_bytes, cudaStream_t st) {
     return check_cuda(cudaLaunchKernelEx(&cfg, kern, p), "linear_hp launch");
 }
 
-template <int NT, bool F32>
-int launch_skinny(LinearParams& p, int splits, cudaStream_t st) {
-    void (*kern)(LinearParams, int) = skinny_kernel<NT, F32>;
-    constexpr size_t smem = sizeof(SkinnySmem<NT>) + 1024;
-    static_assert(smem <= 232448, "shared memory budget");
+// A launch of skinny_kernel: tokens per tile, ring slots and K splits.
+struct SkinnyShape {
+    int nt, stages, splits;
+    float us;  // estimated time
+};
+
+// Time estimates in microseconds, fitted to sweeps on one B200 (K, N = 5120 x
+// 5120, 1504 x 4128, 5120 x 1024, 512 x 13824, 1 to 1536 tokens; within about a
+// tenth of the measured times). A launch of skinny_kernel costs 3.6, a CTA alone on
+// its SM takes a K-step of nt tokens in max(0.165, 0.115 + 0.00103 nt) (FP32, with
+// its chunks: max(0.22, 0.13 + 0.00103 nt)) and its tile's end in 0.03 a token; two on an SM take 0.86 of twice the steps and 0.042 a
+// token. Joining split sums costs 1.6, and the weights come at 6.2 TB/s.
+// pair_kernel costs 8.5 and, per round of tiles, 0.29 a K-step, at least 5.2 for the
+// epilogue; FP32 0.4 a K-step and 4.5 for the epilogue, which the sums in registers
+// keep from running under the next tile.
+SkinnyShape skinny_shape(int64_t M, int64_t N, int ksteps, bool f32, int sms) {
+    SkinnyShape best{0, 0, 0, 1e30f};
+    const int64_t ntiles = ceil_div(N, ROWS);
+    const int most = f32 ? 128 : 256;  // an FP32 lane holds its tokens' sums in registers
+    const int64_t fewest = ceil_div(M, most);
+    for (int64_t tiles = fewest; tiles <= fewest + 8 && (tiles == fewest || ceil_div(M, tiles) > 32); ++tiles) {
+        const int nt = static_cast<int>(round_up(ceil_div(M, tiles), 16));
+        const float step = f32 ? std::max(0.22f, 0.13f + 0.00103f * nt) : std::max(0.165f, 0.115f + 0.00103f * nt);
+        for (int splits = 1; splits <= 8 && (splits == 1 || ksteps >= 4 * splits); splits *= 2) {
+            const int64_t ctas = ntiles * ceil_div(M, nt) * splits, per = ceil_div(ksteps, splits);
+            if (splits > 1 && ctas > 2 * sms) break;
+            const bool two = ctas > sms && nt <= 160;  // three ring slots of 160 tokens still fit twice
+            const float rounds = static_cast<float>(ceil_div(ctas, two ? 2 * sms : sms));
+            const float work = rounds * (two ? 1.72f * per * step + 0.042f * nt : per * step + 0.03f * nt);
+            const float us = 3.6f + (splits > 1 ? 1.6f : 0.0f) + std::max(work, static_cast<float>(N) * ksteps * (KSTEP * 2) / 6.2e6f);
+            if (us < best.us) best = SkinnyShape{nt, 0, splits, us};
+        }
+    }
+    // as many slots as two CTAs per SM leave room for (one, where that is all there are); the partial sums
+    // take the ring's place
+    const int64_t ctas = ntiles * ceil_div(M, best.nt) * best.splits;
+    const int slot = sk_slot(best.nt), room = ctas <= sms ? 208 * 1024 : 108 * 1024;
+    best.stages = std::min(SK_MAX_STAGES, std::max(room / slot, static_cast<int>(ceil_div(best.nt * ROWS * 4, slot))));
+    return best;
+}
+
+float pair_us(int64_t M, int64_t N, int ksteps, bool f32, int sms) {
+    const int64_t tiles = ceil_div(M, 256) * ceil_div(N, PK_N);
+    return 8.5f + static_cast<float>(ceil_div(tiles, sms / 2)) * (f32 ? 0.4f * ksteps + 4.5f : std::max(5.2f, 0.29f * ksteps));
+}
+
+template <int SUMS>
+int launch_skinny(LinearParams& p, const SkinnyShape& s, cudaStream_t st) {
+    void (*kern)(LinearParams, int, int, int, uint32_t) = skinny_kernel<SUMS>;
+    const size_t smem = static_cast<size_t>(s.stages) * sk_slot(s.nt) + 1024;
     static KernelInfo info[64];
     static std::mutex mu;
     int dev = 0;
     OSM_TRY(current_device(&dev));
-    KernelInfo& ki = info[dev];
     {
         std::lock_guard<std::mutex> lk(mu);
-        if (!ki.ready) {
-            OSM_TRY(check_cuda(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                    static_cast<int>(smem)), "linear_hp smem attribute"));
-            ki.ready = true;
+        if (!info[dev].ready) {
+            OSM_TRY(check_cuda(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024),
+                               "linear_hp smem attribute"));
+            info[dev].ready = true;
         }
     }
-    const int64_t mtiles = ceil_div(p.end.M, NT);
+    const int64_t mtiles = ceil_div(p.end.M, s.nt);
     if (mtiles > 65535) return fail(OSM_ERR_UNSUPPORTED, "linear_hp: too many token tiles");
+    uint32_t acc_cols = 32;
+    while (acc_cols < static_cast<uint32_t>(s.nt)) acc_cols *= 2;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(p.end.N, ROWS) * splits), static_cast<unsigned>(mtiles), 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(p.end.N, ROWS) * s.splits), static_cast<unsigned>(mtiles), 1);
     cfg.blockDim = dim3(SK_THREADS, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
@@ -702,12 +765,12 @@ int launch_skinny(LinearParams& p, int splits, cudaStream_t st) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(splits);
+    attr[1].val.clusterDim.x = static_cast<unsigned>(s.splits);
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = splits > 1 ? 2 : 1;
-    return check_cuda(cudaLaunchKernelEx(&cfg, kern, p, splits), "linear_hp launch");
+    cfg.numAttrs = s.splits > 1 ? 2 : 1;
+    return check_cuda(cudaLaunchKernelEx(&cfg, kern, p, s.splits, s.nt, s.stages, acc_cols), "linear_hp launch");
 }
 
 }  // namespace
@@ -721,30 +784,30 @@ int launch_linear_hp(const osm_plan* pl, const uint16_t* X, int64_t M, const uin
     p.wait_limit_ns = pl->wait_limit_ns;
     p.ksteps = static_cast<int>(pl->kp / KSTEP);
     const bool f32 = y_dtype == OSM_DT_F32;
-    const int64_t ntiles = ceil_div(pl->N, ROWS);
-    // Tokens per tile: the smallest width that takes them all, up to 256; from
-    // there on CTA pairs, once their tiles fill the GPU.
-    const int64_t pair_tiles = ceil_div(M, 256) * ceil_div(pl->N, PK_N);
-    const bool pair = M > 256 && pair_tiles >= 74;
-    int nt = M <= 16 ? 16 : (M <= 32 ? 32 : (M <= 64 || f32 ? 64 : 128));
-    // K is split until the CTAs cover the SMs, each rank keeping four K-steps or more.
-    int splits = 1;
-    const int64_t ctas = ntiles * ceil_div(M, nt);
-    while (splits < 8 && ctas * splits < 148 && p.ksteps / (2 * splits) >= 4) splits *= 2;
+    int dev = 0;
+    OSM_TRY(current_device(&dev));
+    static std::atomic<int> sm_count[64];
+    int sms = sm_count[dev].load(std::memory_order_relaxed);
+    if (!sms) {
+        OSM_TRY(check_cuda(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev), "SM count"));
+        sm_count[dev].store(sms, std::memory_order_relaxed);
+    }
+    // CTA pairs once there are tokens for more than one of their tiles and
+    // they are expected to be done first.
+    bool pair = M > 4096;
+    SkinnyShape shape{};
+    if (!pair) {
+        shape = skinny_shape(M, pl->N, p.ksteps, f32, sms);
+        pair = M > 128 && pair_us(M, pl->N, p.ksteps, f32, sms) < shape.us;
+    }
     const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
-    OSM_TRY(make_map(&p.tm_x, bf, X, pl->K, M, pl->K * 2, KSTEP, pair ? ROWS : nt, sw, "X"));
+    OSM_TRY(make_map(&p.tm_x, bf, X, pl->K, M, pl->K * 2, KSTEP, pair ? ROWS : shape.nt, sw, "X"));
     OSM_TRY(make_map(&p.tm_w, bf, w_hp, pl->kp, pl->N, pl->kp * 2, KSTEP, ROWS, sw, "w_hp"));
     if (pair) return launch_pair(p, f32, pl->N * pl->kp * 2, st);
-    if (f32) {
-        if (nt == 16) return launch_skinny<16, true>(p, splits, st);
-        if (nt == 32) return launch_skinny<32, true>(p, splits, st);
-        return launch_skinny<64, true>(p, splits, st);
-    }
-    if (nt == 16) return launch_skinny<16, false>(p, splits, st);
-    if (nt == 32) return launch_skinny<32, false>(p, splits, st);
-    if (nt == 64) return launch_skinny<64, false>(p, splits, st);
-    return launch_skinny<128, false>(p, splits, st);
+    if (!f32) return launch_skinny<0>(p, shape, st);
+    if (shape.nt <= 32) return launch_skinny<32>(p, shape, st);
+    return shape.nt <= 64 ? launch_skinny<64>(p, shape, st) : launch_skinny<128>(p, shape, st);
 }
 
 }  // namespace osm
