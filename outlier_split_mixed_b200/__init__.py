@@ -136,6 +136,9 @@ def _stream(stream):
 
 def _ptr(t, name, dtypes=None, numel=None, allow_none=False):
     """Device pointer of a contiguous CUDA tensor (or None)."""
+    if (t is not None and t.is_cuda and t.is_contiguous() and (dtypes is None or t.dtype in dtypes)
+            and (numel is None or t.nbytes >= numel)):
+        return t.data_ptr()
     if t is None:
         if allow_none:
             return None
@@ -453,14 +456,15 @@ def dual_gemm(plan: Plan, a_codes, a_scales, a_hp, M: int, w_codes, w_scales, w_
                                    _ptr(nh, "next_hp", _bf16_types(), nhb, allow_none=nhb == 0), _stream(stream)))
         return
     ybytes = M * plan.N * (4 if epi == EPI_F32 else 2)
-    ytypes = (torch.float32,) if epi == EPI_F32 else _bf16_types()
+    u8, bf = _u8_types(), _bf16_types()
+    ytypes = (torch.float32,) if epi == EPI_F32 else bf
     _check(lib().osm_dual_gemm(plan.handle,
-                               _ptr(a_codes, "a_codes", _u8_types(), cbm, allow_none=cbm == 0),
-                               _ptr(a_scales, "a_scales", _u8_types(), sbm, allow_none=sbm == 0),
-                               _ptr(a_hp, "a_hp", _bf16_types(), hbm, allow_none=hbm == 0), M,
-                               _ptr(w_codes, "w_codes", _u8_types(), cbn, allow_none=cbn == 0),
-                               _ptr(w_scales, "w_scales", _u8_types(), sbn, allow_none=sbn == 0),
-                               _ptr(w_hp, "w_hp", _bf16_types(), hbn, allow_none=hbn == 0),
+                               _ptr(a_codes, "a_codes", u8, cbm, allow_none=cbm == 0),
+                               _ptr(a_scales, "a_scales", u8, sbm, allow_none=sbm == 0),
+                               _ptr(a_hp, "a_hp", bf, hbm, allow_none=hbm == 0), M,
+                               _ptr(w_codes, "w_codes", u8, cbn, allow_none=cbn == 0),
+                               _ptr(w_scales, "w_scales", u8, sbn, allow_none=sbn == 0),
+                               _ptr(w_hp, "w_hp", bf, hbn, allow_none=hbn == 0),
                                _ptr(bias, "bias", (torch.float32,), plan.N * 4, allow_none=True), int(epi),
                                _ptr(Y, "Y", ytypes, ybytes), None, None, None, None, _stream(stream)))
 
@@ -627,10 +631,10 @@ def _shared_rows(t, name, M, D, rows, dev):
     if t is None:
         return None, 1, 0
     s = t.shape
-    if len(s) not in (1, 2) or t.dtype not in _types["f32"] or not t.is_cuda:
+    if len(s) not in (1, 2) or t.dtype not in _types["f32"] or t.get_device() != dev:
+        if t.is_cuda and t.dtype in _types["f32"] and len(s) in (1, 2):
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
         raise ValueError(f"{name} must be a float32 CUDA tensor [D] or [B][D]")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
     stride = t.stride()
     if s[-1] != D or stride[-1] != 1:
         raise ValueError(f"{name} needs {D} contiguous columns")
@@ -657,20 +661,26 @@ class Norm:
         _stream_types()
         if dev is None:
             dev = self._any_device()
-        scale, rows, stride = _shared_rows(self.scale, "scale", M, D, self.mod_rows, dev)
-        shift, rows2, stride2 = _shared_rows(self.shift, "shift", M, D, self.mod_rows, dev)
-        if self.scale is None:
-            rows, stride = rows2, stride2
-        elif self.shift is not None and (rows2 != rows or (rows < M and stride2 != stride)):
-            raise ValueError("scale and shift must have the same rows and row stride")
+        a, b = self.scale, self.shift
+        scale, rows, stride = _shared_rows(a, "scale", M, D, self.mod_rows, dev)
+        if b is None:
+            shift = None
+        elif a is not None and b.shape == a.shape and b.stride() == a.stride() and b.dtype == a.dtype and b.device == a.device:
+            shift = b.data_ptr()
+        else:
+            shift, rows2, stride2 = _shared_rows(b, "shift", M, D, self.mod_rows, dev)
+            if a is None:
+                rows, stride = rows2, stride2
+            elif rows2 != rows or (rows < M and stride2 != stride):
+                raise ValueError("scale and shift must have the same rows and row stride")
         return _NormSpec(self.kind, self.eps, _vector(self.weight, "weight", D, dev), _vector(self.bias, "bias", D, dev),
                          scale, shift, rows, stride)
 
     def _any_device(self) -> int:
         for t in (self.scale, self.shift, self.weight, self.bias):
-            if t is not None:
+            if t is not None and t.is_cuda:
                 return t.get_device()
-        return -1
+        return -2  # no device: tensors of the host are refused
 
 
 def _new(shape, dtype, like, stream):
@@ -686,14 +696,13 @@ def _new(shape, dtype, like, stream):
 def norm_modulate(X, norm: Norm, out=None, stream=None):
     """H = bf16(norm(X)) (osm_norm_modulate). X: [M][D] BF16 or float32; out: [M][D] BF16 (may be X)."""
     M, D = shape = X.shape
-    types = _stream_types()
-    _stream_type(X, "X")
-    _ptr(X, "X")
-    dev = _device()
+    code = _stream_type(X, "X")
+    dev = _device() if X.is_cuda else -2
     bf = _types["bf16 alone"]
+    x = _operand(X, "X", _types["stream"], shape, dev)
     if out is None:
         out = _new(shape, bf[0], X, stream)
-    _check(lib().osm_norm_modulate(_operand(X, "X", types, shape, dev), types[X.dtype], M, D,
+    _check(lib().osm_norm_modulate(x, code, M, D,
                                    ctypes.byref(norm.spec(M, D, dev)), _operand(out, "out", bf, shape, dev),
                                    _stream(stream)))
     return out
@@ -707,15 +716,15 @@ def residual_norm(R, Y, gate=None, gate_rows: int | None = None, alpha: float = 
     code = _stream_type(R, "R")
     if pre is None and h is not None:
         raise ValueError("h goes with pre")
-    _ptr(R, "R")
-    dev = _device()
+    dev = _device() if R.is_cuda else -2
     own, bf = (R.dtype,), _types["bf16 alone"]
+    r = _operand(R, "R", own, shape, dev)
     if out is None:
         out = _new(shape, R.dtype, R, stream)
     if pre is not None and h is None:
         h = _new(shape, bf[0], R, stream)
     g, rows, stride = _shared_rows(gate, "gate", M, D, gate_rows, dev)
-    _check(lib().osm_residual_norm(_operand(R, "R", own, shape, dev), code, _operand(Y, "Y", bf, shape, dev), M, D,
+    _check(lib().osm_residual_norm(r, code, _operand(Y, "Y", bf, shape, dev), M, D,
                                    None if post is None else ctypes.byref(post.spec(M, D, dev)), g, rows, stride, alpha,
                                    None if pre is None else ctypes.byref(pre.spec(M, D, dev)),
                                    _operand(out, "out", own, shape, dev),
@@ -725,9 +734,14 @@ def residual_norm(R, Y, gate=None, gate_rows: int | None = None, alpha: float = 
 
 def _packed_ptrs(plan: Plan, rows: int, codes, scales, hp, which: str, dev: int):
     """Addresses of packed operands, with their sizes checked."""
+    cb, sb, hb = plan.sizes(rows)
+    u8, bf = _u8_types(), _bf16_types()
+    if cb and hb:  # the usual layer: bulk and outlier channels
+        got = _ptr(codes, f"{which}_codes", u8, cb), _ptr(scales, f"{which}_scales", u8, sb), _ptr(hp, f"{which}_hp", bf, hb)
+        if codes.get_device() == dev and scales.get_device() == dev and hp.get_device() == dev:
+            return got
     got = []
-    for t, n, types, name in zip((codes, scales, hp), plan.sizes(rows), (_u8_types(), _u8_types(), _bf16_types()),
-                                 ("codes", "scales", "hp")):
+    for t, n, types, name in ((codes, cb, u8, "codes"), (scales, sb, u8, "scales"), (hp, hb, bf, "hp")):
         if n == 0 and (t is None or t.numel() == 0):
             got.append(None)
             continue
