@@ -17,6 +17,7 @@
 
 #include "osm_internal.h"
 #include "osm_norm.cuh"
+#include "osm_ptx.cuh"
 
 namespace osm {
 namespace {
@@ -156,15 +157,15 @@ __device__ __forceinline__ void one_row(const RowParams& p, uint32_t row, int j,
     }
 }
 
-// Many rows: a CTA of 16 warps takes a tile of rows of one run, teams of W
+// Many rows: a CTA takes a tile of rows of one run, teams of W
 // warps a row each. The run's coefficients are laid out once per tile in
 // shared memory (FP32, four 16-byte words of a chunk in arrays of their own:
 // conflict-free 128-bit reads), where all teams read them.
-constexpr int ROWS_THREADS = 512;
-
-template <bool F32, bool HAS_Y, int W, int NS, int MINB>
-__global__ void __launch_bounds__(ROWS_THREADS, MINB) rows_kernel(const __grid_constant__ RowParams p) {
-    constexpr int TEAMS = ROWS_THREADS / 32 / W;
+template <bool F32, bool HAS_Y, int W, int NS, int WARPS, int MINB>
+__global__ void __launch_bounds__(32 * WARPS, MINB) rows_kernel(const __grid_constant__ RowParams p) {
+    constexpr int TEAMS = WARPS / W;
+    ptx::grid_dep_wait();    // launched while the kernel before it finishes
+    ptx::grid_dep_launch();
     extern __shared__ __align__(16) uint8_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int team = warp / W, j = warp % W;
@@ -204,7 +205,7 @@ __global__ void __launch_bounds__(ROWS_THREADS, MINB) rows_kernel(const __grid_c
             if (held != 0xffffffffu) __syncthreads();  // the rows of the last run are done
             held = run;
             // word w of chunk c: columns 8c + 4 (w & 1) .. + 3 of a (w < 2) or b
-            for (int i = threadIdx.x; i < ntab / 2 * nchunk; i += ROWS_THREADS) {
+            for (int i = threadIdx.x; i < ntab / 2 * nchunk; i += 32 * WARPS) {
                 const int k = i / nchunk, c = i - k * nchunk;  // k: table * 2 + half
                 const int col = c * norm::CHUNK + 4 * (k & 1);
                 float2 a0, a1, b0, b1;
@@ -232,6 +233,8 @@ __global__ void __launch_bounds__(ROWS_THREADS, MINB) rows_kernel(const __grid_c
 template <bool F32, bool HAS_Y, int NS, int MINB>
 __global__ void __launch_bounds__(512, MINB) row_kernel(const __grid_constant__ RowParams p) {
     __shared__ float part[2][16 * NS];
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
     const int lane = threadIdx.x & 31, j = threadIdx.x >> 5, nw = blockDim.x >> 5;
     const int nseg = (p.D + norm::SEG - 1) / norm::SEG;
     const float inv_d = __frcp_rn(static_cast<float>(p.D));
@@ -290,21 +293,36 @@ int prepare(Setup& su, const void* kern, int threads, size_t smem, int* ctas) {
     return OSM_OK;
 }
 
-template <bool F32, bool HAS_Y, int W, int NS, int MINB>
+// A launch that may start while the kernel before it on the stream finishes.
+template <class K>
+int launch(K kern, unsigned grid, unsigned threads, size_t smem, cudaStream_t st, const RowParams& p) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return check_cuda(cudaLaunchKernelEx(&cfg, kern, p), "norm launch");
+}
+
+template <bool F32, bool HAS_Y, int W, int NS, int WARPS, int MINB>
 int launch_tiles(RowParams p, cudaStream_t st) {
     static Setup su;
-    auto kern = rows_kernel<F32, HAS_Y, W, NS, MINB>;
-    const size_t smem = ROWS_THREADS / 32 / W * 2 * W * NS * 4 +
+    auto kern = rows_kernel<F32, HAS_Y, W, NS, WARPS, MINB>;
+    const size_t smem = WARPS / W * 2 * W * NS * 4 +
                         static_cast<size_t>((HAS_Y ? 4 : 0) + (p.pre.kind >= 0 ? 4 : 0)) * (p.D / norm::CHUNK) * 16;
     int ctas = 0;
-    OSM_TRY(prepare(su, reinterpret_cast<const void*>(kern), ROWS_THREADS, smem, &ctas));
+    OSM_TRY(prepare(su, reinterpret_cast<const void*>(kern), 32 * WARPS, smem, &ctas));
     // one tile per CTA: each run is cut into its part of them
     const int64_t cuts = std::max<int64_t>(1, static_cast<int64_t>(ctas) * p.share / p.M);
     p.tile_rows = static_cast<uint32_t>(ceil_div(p.share, cuts));
     p.tiles_per_run = static_cast<uint32_t>(ceil_div(p.share, p.tile_rows));
     p.tiles = static_cast<uint32_t>(ceil_div(p.M, p.share)) * p.tiles_per_run;
-    kern<<<std::min<uint32_t>(p.tiles, ctas), ROWS_THREADS, smem, st>>>(p);
-    return check_cuda(cudaGetLastError(), "norm launch");
+    return launch(kern, std::min<uint32_t>(p.tiles, ctas), 32 * WARPS, smem, st, p);
 }
 
 template <bool F32, bool HAS_Y, int NS, int MINB>
@@ -314,14 +332,13 @@ int launch_single(const RowParams& p, cudaStream_t st) {
     const int threads = 32 * static_cast<int>(std::min<int64_t>(16, ceil_div(p.D, norm::SEG)));
     int ctas = 0;
     OSM_TRY(prepare(su, reinterpret_cast<const void*>(kern), threads, 0, &ctas));
-    kern<<<std::min<uint32_t>(p.M, ctas), threads, 0, st>>>(p);
-    return check_cuda(cudaGetLastError(), "norm launch");
+    return launch(kern, std::min<uint32_t>(p.M, ctas), threads, 0, st, p);
 }
 
 template <bool F32, bool HAS_Y>
 int launch_width(const RowParams& p, cudaStream_t st) {
-    // Tiles pay once a CTA has a row for each of its 16 warps (M from about
-    // 2400 rows on) and runs long enough to lay out their coefficients once.
+    // Tiles pay once a CTA has about 16 rows (M from about 2400 rows on) and
+    // runs long enough to lay out their coefficients once.
     // The coefficients of 14336 columns (both tables) fill shared memory.
     const bool tiles = p.M >= 148 * 16 && p.share >= 64 && p.D <= 14336;
     if (!tiles) {
@@ -329,15 +346,26 @@ int launch_width(const RowParams& p, cudaStream_t st) {
         if (p.D <= 16384) return launch_single<F32, HAS_Y, 4, F32 ? 1 : 2>(p, st);
         return launch_single<F32, HAS_Y, 16, 1>(p, st);
     }
-    if (p.D <= 512) return launch_tiles<F32, HAS_Y, 1, 2, 2>(p, st);
-    if (p.D <= 2048) return launch_tiles<F32, HAS_Y, 1, 8, 1>(p, st);
-    // warps per row: the row's words of a lane stay within its 128 registers
-    constexpr int W = F32 ? (HAS_Y ? 4 : 2) : (HAS_Y ? 2 : 1);
-    if (p.D <= 5120) return launch_tiles<F32, HAS_Y, W, 20 / W, 1>(p, st);
+    // Warps per row and per CTA, by what a lane holds of a row (8 columns of each
+    // of NS segments: 4 registers for BF16, 8 for FP32, 4 more for y), measured at
+    // 2048 and 5120 columns: fewer registers and more warps until the totals'
+    // barriers and shuffles cost more than the latency that they hide. 32760 x 5120
+    // BF16 in us, norm_modulate: 1 warp of 20 segments and 16 warps per CTA 127.5, 2
+    // x 10 122.0, 4 x 5 and 28 warps 119.2; residual_norm: 2 x 10 and 16 warps 242.1,
+    // 4 x 5 and 24 warps 237.2, 28 warps 252 (spills).
+    if (p.D <= 512) return launch_tiles<F32, HAS_Y, 1, 2, 16, 2>(p, st);
+    if (p.D <= 2048) {
+        if constexpr (HAS_Y) return launch_tiles<F32, HAS_Y, 2, 4, 24, 1>(p, st);
+        else return launch_tiles<F32, HAS_Y, 2, 4, 16, 2>(p, st);
+    }
+    if (p.D <= 5120) {
+        if constexpr (F32) return launch_tiles<F32, HAS_Y, HAS_Y ? 4 : 2, HAS_Y ? 5 : 10, 16, 1>(p, st);
+        else return launch_tiles<F32, HAS_Y, 4, 5, HAS_Y ? 24 : 28, 1>(p, st);
+    }
     constexpr int V = F32 || HAS_Y ? 4 : 2;
-    if (p.D <= 8192) return launch_tiles<F32, HAS_Y, V, 32 / V, 1>(p, st);
+    if (p.D <= 8192) return launch_tiles<F32, HAS_Y, V, 32 / V, 16, 1>(p, st);
     constexpr int U = F32 || HAS_Y ? 8 : 4;
-    return launch_tiles<F32, HAS_Y, U, 56 / U, 1>(p, st);
+    return launch_tiles<F32, HAS_Y, U, 56 / U, 16, 1>(p, st);
 }
 
 Spec to_spec(const osm_norm_spec* s) {

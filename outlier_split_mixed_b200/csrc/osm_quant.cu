@@ -1083,6 +1083,7 @@ __device__ __forceinline__ uint32_t norm_smooth2(float2 x, float2 st, float2 a, 
 template <int MODE, bool F32>
 __global__ void __launch_bounds__(QA_THREADS) norm_quantize_kernel(QuantParams p, norm::Spec s, const void* X) {
     constexpr bool HPF = MODE == QA_MX_F16;
+    ptx::grid_dep_wait();    // launched while the kernel before it finishes
     ptx::grid_dep_launch();  // the dual_gemm that follows may start its prologue
     extern __shared__ __align__(128) uint8_t smem[];
     const int nb = p.Kbp >> 5, nchunk = p.K / norm::CHUNK, nseg = (p.K + norm::SEG - 1) / norm::SEG;
@@ -1232,6 +1233,7 @@ __global__ void __launch_bounds__(NormQuantShape<W, NS>::THREADS, MINB)
     constexpr bool HPF = MODE == QA_MX_F16;
     constexpr int R = F32 ? 1 : 2;
     constexpr int XQ = F32 ? 2 : 1;
+    ptx::grid_dep_wait();    // launched while the kernel before it finishes
     ptx::grid_dep_launch();  // the dual_gemm that follows may start its prologue
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, team = warp / W, j = warp % W, tt = tid % (32 * W);
@@ -1585,6 +1587,22 @@ static QuantParams quant_params(const osm_plan* pl, const uint16_t* X, int64_t M
                   pow2f(-pl->g_act)};
 }
 
+// A launch that may start while the kernel before it on the stream finishes.
+template <class K, class... A>
+static int launch_dependent(K kern, unsigned grid, unsigned threads, size_t smem, cudaStream_t st, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return check_cuda(cudaLaunchKernelEx(&cfg, kern, args...), "norm_quantize_act launch");
+}
+
 template <int W, int NS, int MINB>
 static int launch_norm_quantize_rows(const QuantParams& p, int mode, const norm::Spec& s, const void* X, bool f32, int64_t M,
                                      int64_t run, cudaStream_t st) {
@@ -1605,10 +1623,9 @@ static int launch_norm_quantize_rows(const QuantParams& p, int mode, const norm:
     const int64_t cuts = ctas * run / M > 1 ? ctas * run / M : 1;
     const int64_t tile_rows = ceil_div(run, cuts), per_run = ceil_div(run, tile_rows);
     const int64_t tiles = ceil_div(M, run) * per_run;
-    kern<<<static_cast<unsigned>(tiles < ctas ? tiles : ctas), NormQuantShape<W, NS>::THREADS, smem, st>>>(
-        p, s, X, static_cast<uint32_t>(run), static_cast<uint32_t>(tile_rows), static_cast<uint32_t>(per_run),
-        static_cast<uint32_t>(tiles));
-    return check_cuda(cudaGetLastError(), "norm_quantize_act launch");
+    return launch_dependent(kern, static_cast<unsigned>(tiles < ctas ? tiles : ctas), NormQuantShape<W, NS>::THREADS, smem,
+                            st, p, s, X, static_cast<uint32_t>(run), static_cast<uint32_t>(tile_rows),
+                            static_cast<uint32_t>(per_run), static_cast<uint32_t>(tiles));
 }
 
 int launch_norm_quantize(const osm_plan* pl, const void* X, int x_dtype, int64_t M, const osm_norm_spec* spec,
@@ -1638,8 +1655,7 @@ int launch_norm_quantize(const osm_plan* pl, const void* X, int x_dtype, int64_t
     if (rc) return rc;
     if (per_sm < 1) return fail(OSM_ERR_UNSUPPORTED, "norm_quantize_act: no CTA fits (K = %lld)", (long long)pl->K);
     const int64_t grid = M < static_cast<int64_t>(sms) * per_sm ? M : static_cast<int64_t>(sms) * per_sm;
-    kern<<<static_cast<unsigned>(grid), QA_THREADS, smem, st>>>(p, s, X);
-    return check_cuda(cudaGetLastError(), "norm_quantize_act launch");
+    return launch_dependent(kern, static_cast<unsigned>(grid), QA_THREADS, smem, st, p, s, X);
 }
 
 int launch_quantize_act(const osm_plan* pl, const uint16_t* X, int64_t M, uint8_t* codes,
