@@ -113,9 +113,13 @@ struct Tile {
             if (j < nj && rb < p.M) w[2 * j + 1] = pb[4 * j];
         }
     }
-    // Slab sl (0, 1) from its 64 accumulator registers.
+    // Slab sl (0, 1) from its 64 accumulator registers, which are used up: four
+    // 8-column blocks per turn of a rolled loop, after which registers and
+    // residual words move down (they cannot be indexed at run time). Unrolled,
+    // the loop's code took several microseconds to fetch the first time (a
+    // 256-token F32 call: 7 of its 13 us).
     template <bool SCALED, bool ACT>
-    __device__ __forceinline__ void store(const Params& p, int sl, int lane, const Vectors& v, const uint32_t* r) {
+    __device__ __forceinline__ void store(const Params& p, int sl, int lane, const Vectors& v, uint32_t* r) {
         const int64_t ra = y0 + 16 * sl + (lane >> 2), rb = ra + 8, c0 = x0 + 2 * (lane & 3);
         const bool on_a = ra < p.M, on_b = rb < p.M, more = p.onto.r != nullptr && sl == 0;
         const bool next_a = more && ra + 16 < p.M, next_b = more && rb + 16 < p.M;
@@ -130,36 +134,58 @@ struct Tile {
         Word<F32>* oa = at(p.Y, p, ra, c0);
         const float2* vb = reinterpret_cast<const float2*>(v.bias) + (lane & 3);
         const float2* vg = reinterpret_cast<const float2*>(v.gate) + (lane & 3);
+#pragma unroll 1
+        for (int j0 = 0; j0 < nj; j0 += 4) {  // nj is a multiple of 4 (N % 32 == 0)
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            if (j >= nj) break;
-            float2 a = make_float2(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]));
-            float2 b = make_float2(__uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
-            if constexpr (SCALED) {
-                a = __fmul2_rn(a, make_float2(p.scale, p.scale));
-                b = __fmul2_rn(b, make_float2(p.scale, p.scale));
+            for (int i = 0; i < 4; ++i) {
+                float2 a = make_float2(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]));
+                float2 b = make_float2(__uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3]));
+                if constexpr (SCALED) {
+                    a = __fmul2_rn(a, make_float2(p.scale, p.scale));
+                    b = __fmul2_rn(b, make_float2(p.scale, p.scale));
+                }
+                if (p.bias) {
+                    a = __fadd2_rn(a, vb[4 * i]);
+                    b = __fadd2_rn(b, vb[4 * i]);
+                }
+                if constexpr (ACT) {
+                    a = activate2(a, p.act);
+                    b = activate2(b, p.act);
+                }
+                if (p.onto.gate) {
+                    a = __fmul2_rn(a, staged ? vg[4 * i] : __ldg(reinterpret_cast<const float2*>(gate_a + 8 * i)));
+                    b = __fmul2_rn(b, staged ? vg[4 * i] : __ldg(reinterpret_cast<const float2*>(gate_b + 8 * i)));
+                }
+                if (p.onto.r) {
+                    a = __fadd2_rn(from_word<F32>(w[2 * i]), a);
+                    b = __fadd2_rn(from_word<F32>(w[2 * i + 1]), b);
+                }
+                if (on_a) oa[4 * i] = to_word<F32>(a);
+                if (on_b) oa[step + 4 * i] = to_word<F32>(b);
             }
-            if (p.bias) {
-                a = __fadd2_rn(a, vb[4 * j]);
-                b = __fadd2_rn(b, vb[4 * j]);
-            }
-            if constexpr (ACT) {
-                a = activate2(a, p.act);
-                b = activate2(b, p.act);
-            }
-            if (p.onto.gate) {
-                a = __fmul2_rn(a, staged ? vg[4 * j] : __ldg(reinterpret_cast<const float2*>(gate_a + 8 * j)));
-                b = __fmul2_rn(b, staged ? vg[4 * j] : __ldg(reinterpret_cast<const float2*>(gate_b + 8 * j)));
-            }
+#pragma unroll
+            for (int e = 0; e < 48; ++e) r[e] = r[e + 16];
             if (p.onto.r) {
-                a = __fadd2_rn(from_word<F32>(w[2 * j]), a);
-                b = __fadd2_rn(from_word<F32>(w[2 * j + 1]), b);
-                if (next_a) w[2 * j] = na[4 * j];
-                if (next_b) w[2 * j + 1] = na[step + 4 * j];
+#pragma unroll
+                for (int e = 0; e < 24; ++e) w[e] = w[e + 8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {  // the next slab's words of these blocks queue up behind
+                    if (next_a) w[24 + 2 * i] = na[4 * i];
+                    if (next_b) w[25 + 2 * i] = na[step + 4 * i];
+                }
             }
-            if (on_a) oa[4 * j] = to_word<F32>(a);
-            if (on_b) oa[step + 4 * j] = to_word<F32>(b);
+            oa += 16;
+            na += 16;
+            vb += 16;
+            vg += 16;
+            gate_a += 32;
+            gate_b += 32;
         }
+        // a slab of fewer blocks leaves the queue's head in the wrong place
+        if (more)
+            for (int j = nj; j < 16; j += 4)
+#pragma unroll
+                for (int e = 0; e < 24; ++e) w[e] = w[e + 8];
     }
 };
 
