@@ -104,13 +104,14 @@ struct Tile {
     // The first slab's residual words; before the wait for the accumulator
     // where the registers allow.
     __device__ __forceinline__ void load_first(const Params& p, int lane) {
-        if (!p.onto.r) return;
         const int64_t ra = y0 + (lane >> 2), rb = ra + 8, col = x0 + 2 * (lane & 3);
         const Word<F32> *pa = at(p.onto.r, p, ra, col), *pb = at(p.onto.r, p, rb, col);
+        const int last = p.onto.r ? nj : 0;
+        // every word is set, so that none occupies a register before
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-            if (j < nj && ra < p.M) w[2 * j] = pa[4 * j];
-            if (j < nj && rb < p.M) w[2 * j + 1] = pb[4 * j];
+            w[2 * j] = j < last && ra < p.M ? pa[4 * j] : Word<F32>{};
+            w[2 * j + 1] = j < last && rb < p.M ? pb[4 * j] : Word<F32>{};
         }
     }
     // Slab sl (0, 1) from its 64 accumulator registers, which are used up: four
@@ -170,8 +171,8 @@ struct Tile {
                 for (int e = 0; e < 24; ++e) w[e] = w[e + 8];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {  // the next slab's words of these blocks queue up behind
-                    if (next_a) w[24 + 2 * i] = na[4 * i];
-                    if (next_b) w[25 + 2 * i] = na[step + 4 * i];
+                    w[24 + 2 * i] = next_a ? na[4 * i] : Word<F32>{};
+                    w[25 + 2 * i] = next_b ? na[step + 4 * i] : Word<F32>{};
                 }
             }
             oa += 16;
