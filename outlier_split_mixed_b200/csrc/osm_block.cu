@@ -8,6 +8,8 @@
 
 #include <algorithm>
 #include <cmath>
+#include <exception>
+#include <new>
 
 #include "osm_internal.h"
 
@@ -47,6 +49,18 @@ int check_gate(const char* who, const float* gate, int64_t M, int64_t N, int64_t
     return check_rows(who, "gate", M, N, rows, stride);
 }
 
+// Nothing is thrown across the C boundary.
+template <class F>
+int guarded(F body) {
+    try {
+        return body();
+    } catch (const std::bad_alloc&) {
+        return fail(OSM_ERR_NOMEM, "host allocation failed");
+    } catch (const std::exception& e) {
+        return fail(OSM_ERR_CUDA, "%s", e.what());
+    }
+}
+
 Onto onto_of(const void* R, const float* gate, int64_t gate_rows, int64_t gate_stride, int64_t M) {
     return Onto{R, gate, gate ? std::min(gate_rows, M) : M, gate_stride};
 }
@@ -68,8 +82,10 @@ int osm_norm_modulate(const void* X, int x_dtype, int64_t M, int64_t D, const os
     OSM_REQUIRE(X && aligned16(X) && H && aligned16(H), "norm_modulate: X / H null or misaligned");
     OSM_REQUIRE(x_dtype == OSM_DT_BF16 || X != H, "norm_modulate: an FP32 X cannot be normalised in place");
     OSM_TRY(check_device());
-    return launch_norm_rows(X, x_dtype, M, D, nullptr, nullptr, nullptr, 0, 0, 1.0f, spec, nullptr, H,
-                            static_cast<cudaStream_t>(stream));
+    return guarded([&] {
+        return launch_norm_rows(X, x_dtype, M, D, nullptr, nullptr, nullptr, 0, 0, 1.0f, spec, nullptr, H,
+                                static_cast<cudaStream_t>(stream));
+    });
 }
 
 int osm_residual_norm(const void* R, int r_dtype, const uint16_t* Y, int64_t M, int64_t D, const osm_norm_spec* post,
@@ -92,8 +108,10 @@ int osm_residual_norm(const void* R, int r_dtype, const uint16_t* Y, int64_t M, 
                     static_cast<const void*>(Y) != R_out,
                 "residual_norm: R_out may be R and H may be Y, nothing else");
     OSM_TRY(check_device());
-    return launch_norm_rows(R, r_dtype, M, D, Y, post, gate, gate_rows, gate_stride, alpha, pre, R_out, H,
-                            static_cast<cudaStream_t>(stream));
+    return guarded([&] {
+        return launch_norm_rows(R, r_dtype, M, D, Y, post, gate, gate_rows, gate_stride, alpha, pre, R_out, H,
+                                static_cast<cudaStream_t>(stream));
+    });
 }
 
 int osm_norm_quantize_act(const osm_plan* p, const void* X, int x_dtype, int64_t M, const osm_norm_spec* spec,
@@ -108,7 +126,9 @@ int osm_norm_quantize_act(const osm_plan* p, const void* X, int x_dtype, int64_t
     OSM_REQUIRE(p->Kbp == 0 || (a_codes && aligned16(a_codes) && a_scales && aligned16(a_scales)),
                 "norm_quantize_act: a_codes / a_scales null or misaligned");
     OSM_REQUIRE(p->kp == 0 || (a_hp && aligned16(a_hp)), "norm_quantize_act: a_hp null or misaligned");
-    return launch_norm_quantize(p, X, x_dtype, M, spec, a_codes, a_scales, a_hp, static_cast<cudaStream_t>(stream));
+    return guarded([&] {
+        return launch_norm_quantize(p, X, x_dtype, M, spec, a_codes, a_scales, a_hp, static_cast<cudaStream_t>(stream));
+    });
 }
 
 int osm_dual_gemm_residual(const osm_plan* p, const uint8_t* a_codes, const uint8_t* a_scales, const uint16_t* a_hp,
@@ -129,9 +149,11 @@ int osm_dual_gemm_residual(const osm_plan* p, const uint8_t* a_codes, const uint
                 "dual_gemm_residual: outlier operands null or misaligned");
     OSM_TRY(check_device());
     const Onto onto = onto_of(R, gate, gate_rows, gate_stride, M);
-    return launch_dual_gemm(p, a_codes, a_scales, a_hp, M, w_codes, w_scales, w_hp, bias,
-                            r_dtype == OSM_DT_F32 ? EPI_ONTO_F32 : EPI_ONTO_BF16, Y, nullptr, nullptr, nullptr, nullptr,
-                            static_cast<cudaStream_t>(stream), &onto);
+    return guarded([&] {
+        return launch_dual_gemm(p, a_codes, a_scales, a_hp, M, w_codes, w_scales, w_hp, bias,
+                                r_dtype == OSM_DT_F32 ? EPI_ONTO_F32 : EPI_ONTO_BF16, Y, nullptr, nullptr, nullptr,
+                                nullptr, static_cast<cudaStream_t>(stream), &onto);
+    });
 }
 
 int osm_linear_hp(const osm_plan* p, const uint16_t* X, int64_t M, const uint16_t* w_hp, const float* bias, int act,
@@ -152,8 +174,10 @@ int osm_linear_hp(const osm_plan* p, const uint16_t* X, int64_t M, const uint16_
     OSM_REQUIRE(aligned16(bias) && aligned16(R), "linear_hp: bias / R misaligned");
     OSM_TRY(check_gate("linear_hp", gate, M, p->N, gate_rows, gate_stride));
     OSM_TRY(check_device());
-    return launch_linear_hp(p, X, M, w_hp, bias, act, onto_of(R, gate, gate_rows, gate_stride, M), Y, y_dtype,
-                            static_cast<cudaStream_t>(stream));
+    return guarded([&] {
+        return launch_linear_hp(p, X, M, w_hp, bias, act, onto_of(R, gate, gate_rows, gate_stride, M), Y, y_dtype,
+                                static_cast<cudaStream_t>(stream));
+    });
 }
 
 int osm_ffn_sublayer(const osm_plan* up, const osm_plan* down, const osm_norm_spec* pre, const void* R, int r_dtype,

@@ -200,27 +200,6 @@ __device__ __forceinline__ uint64_t desc_sf(uint32_t saddr) {
     return ptx::smem_desc(saddr, 0, 128, ptx::LAYOUT_NONE);
 }
 
-// Load one 16-lane slab of the accumulator: 16 TMEM lanes x 128 columns.
-// Thread t receives lanes t/4 and t/4 + 8 and, for each 8-column block j,
-// columns 8j + 2(t%4) and 8j + 2(t%4) + 1 (registers 4j .. 4j+3), so the
-// four lanes of a quad hold one row's 32 contiguous bytes.
-__device__ __forceinline__ void tmem_ld_16x256b_x16(uint32_t taddr, uint32_t* r) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x16.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
-        "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
-        "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
-          "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
-          "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
-          "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
-          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
-        : "r"(taddr));
-}
 // Add the bias and store one 16-row x 128-column slab from registers: each
 // store instruction of the warp writes eight full 32-byte sectors (one per
 // row), FP32 as 8-byte pairs or BF16 as 4-byte pairs. Rows >= M and
@@ -609,8 +588,8 @@ __device__ __forceinline__ void epilogue_role(const GemmParams& p, Smem<NV>& S, 
         } else {
             // four lanes per row: full 32-byte sectors per store
             uint32_t r[128];
-            tmem_ld_16x256b_x16(taddr, r);
-            tmem_ld_16x256b_x16(taddr + (16u << 16), r + 64);
+            ptx::tmem_ld_16x256b_x16(taddr, r);
+            ptx::tmem_ld_16x256b_x16(taddr + (16u << 16), r + 64);
             release_accumulator(acc_empty_leader, lane);
             if (x0 < p.N) {
 #pragma unroll 1

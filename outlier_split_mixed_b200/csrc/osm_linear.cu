@@ -107,40 +107,6 @@ __device__ __forceinline__ void pair_coords(const LinearParams& p, int tile, int
     n = local / gm;
 }
 
-// Sixteen tensor-memory lanes x 128 columns: thread t holds rows t / 4 and
-// t / 4 + 8 and, of each 8-column block j, columns 2 (t % 4) and the next
-// (registers 4j .. 4j + 3).
-__device__ __forceinline__ void tmem_ld_16x256b_x16(uint32_t taddr, uint32_t* r) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x16.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
-        "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
-        "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
-          "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
-          "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
-          "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
-          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
-        : "r"(taddr));
-}
-
-// As above, 64 columns (registers 4j .. 4j + 3 of eight blocks).
-__device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t* r) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
-}
-
 template <bool F32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PK_THREADS, 1)
     pair_kernel(const __grid_constant__ LinearParams p) {
@@ -300,14 +266,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PK_THREADS, 1)
                     if (!(ok = wait_full())) break;
                     const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + (it & 1) * PK_N + half * 128;
                     if (k0 == 0) {
-                        tmem_ld_16x256b_x16(taddr, sum);
-                        tmem_ld_16x256b_x16(taddr + (16u << 16), sum + 64);
+                        ptx::tmem_ld_16x256b_x16(taddr, sum);
+                        ptx::tmem_ld_16x256b_x16(taddr + (16u << 16), sum + 64);
                         ptx::tmem_ld_wait();
                     } else {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {  // slab i / 2, columns 64 (i % 2) ..
                             uint32_t r[32];
-                            tmem_ld_16x256b_x8(taddr + (static_cast<uint32_t>(16 * (i >> 1)) << 16) + 64 * (i & 1), r);
+                            ptx::tmem_ld_16x256b_x8(taddr + (static_cast<uint32_t>(16 * (i >> 1)) << 16) + 64 * (i & 1), r);
                             ptx::tmem_ld_wait();
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
@@ -333,7 +299,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PK_THREADS, 1)
 #pragma unroll 1
                 for (int sl = 0; sl < 2; ++sl) {
                     uint32_t r[64];
-                    tmem_ld_16x256b_x16(taddr + (static_cast<uint32_t>(16 * sl) << 16), r);
+                    ptx::tmem_ld_16x256b_x16(taddr + (static_cast<uint32_t>(16 * sl) << 16), r);
                     ptx::tmem_ld_wait();
                     if (sl == 1) release();
                     if (end.nj > 0) end.template store<false, true>(p.end, sl, lane, S.vectors[warp], r);

@@ -11,9 +11,7 @@
 
 #include <algorithm>
 #include <cstdint>
-#include <map>
 #include <mutex>
-#include <utility>
 
 #include "osm_internal.h"
 #include "osm_norm.cuh"
@@ -259,37 +257,44 @@ __global__ void __launch_bounds__(512, MINB) row_kernel(const __grid_constant__ 
     }
 }
 
-// Device, SM count and CTAs per SM of a kernel, looked up once per device,
-// CTA and shared-memory size.
+// Resident CTAs of a kernel on the current device, looked up once per device,
+// CTA size and shared-memory size (the last few shapes are kept).
 struct Setup {
+    struct Shape {
+        size_t smem = ~size_t(0);
+        int threads = 0, ctas = 0;
+    };
     std::mutex mu;
     size_t smem_set[64] = {};
-    std::map<std::pair<size_t, int>, int> per_sm[64];
+    Shape shapes[64][8];
+    int next[64] = {};
 };
 int prepare(Setup& su, const void* kern, int threads, size_t smem, int* ctas) {
-    static int sms[64] = {};
     int dev = 0, rc;
     if ((rc = check_cuda(cudaGetDevice(&dev), "cudaGetDevice"))) return rc;
     if (dev < 0 || dev >= 64) return fail(OSM_ERR_UNSUPPORTED, "device index %d", dev);
     std::lock_guard<std::mutex> lk(su.mu);
+    for (const Setup::Shape& s : su.shapes[dev])
+        if (s.smem == smem && s.threads == threads) {
+            *ctas = s.ctas;
+            return OSM_OK;
+        }
     if (smem > 48 * 1024 && su.smem_set[dev] < smem) {
         if ((rc = check_cuda(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                   static_cast<int>(smem)), "norm smem attribute")))
             return rc;
         su.smem_set[dev] = smem;
     }
-    auto it = su.per_sm[dev].find({smem, threads});
-    if (it == su.per_sm[dev].end()) {
-        int n = 0;
-        if ((rc = check_cuda(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, smem), "norm occupancy")))
-            return rc;
-        if (n < 1) return fail(OSM_ERR_UNSUPPORTED, "norm: no CTA fits");
-        int s = 0;
-        if ((rc = check_cuda(cudaDeviceGetAttribute(&s, cudaDevAttrMultiProcessorCount, dev), "SM count"))) return rc;
-        sms[dev] = s;
-        it = su.per_sm[dev].emplace(std::make_pair(smem, threads), n).first;
-    }
-    *ctas = it->second * sms[dev];
+    int n = 0, sms = 0;
+    if ((rc = check_cuda(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, smem), "norm occupancy")))
+        return rc;
+    if (n < 1) return fail(OSM_ERR_UNSUPPORTED, "norm: no CTA fits");
+    if ((rc = check_cuda(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev), "SM count"))) return rc;
+    Setup::Shape& s = su.shapes[dev][su.next[dev]];
+    su.next[dev] = (su.next[dev] + 1) % 8;
+    s.smem = smem;
+    s.threads = threads;
+    s.ctas = *ctas = n * sms;
     return OSM_OK;
 }
 

@@ -29,11 +29,11 @@ struct Params {
     int act;             // OSM_ACT_* (used by ACT kernels)
 };
 
-// x / (1 + 2^z) with z = -x log2(e); z is capped so that 1 + 2^z stays finite.
+// x / (1 + 2^z) with z = -x log2(e), 2^z and the reciprocal on the special-
+// function unit. Where 2^z overflows the reciprocal is 0 and the result -0.
 __device__ __forceinline__ float2 silu2(float2 x) {
     const float2 z = __fmul2_rn(x, make_float2(-1.44269504f, -1.44269504f));
-    const float2 d = __fadd2_rn(make_float2(mx::ex2_approx(fminf(z.x, 126.0f)), mx::ex2_approx(fminf(z.y, 126.0f))),
-                                make_float2(1.0f, 1.0f));
+    const float2 d = __fadd2_rn(make_float2(mx::ex2_approx(z.x), mx::ex2_approx(z.y)), make_float2(1.0f, 1.0f));
     return __fmul2_rn(x, make_float2(mx::rcp_approx(d.x), mx::rcp_approx(d.y)));
 }
 __device__ __forceinline__ float2 activate2(float2 v, int act) {

@@ -396,6 +396,100 @@ def test_linear_hp_reports_a_wait_that_runs_out(M):
     assert lin.plan.status() == 0
 
 
+def test_linear_hp_keeps_nonfinite_rows_to_themselves():
+    g = gen(8)
+    lin = osm.HpLinear(rand(g, 512, 384, dtype=BF, scale=0.05), rand(g, 384))
+    for M in (7, 300, 3000):
+        x, r = rand(g, M, 512, dtype=BF), rand(g, M, 384)
+        clean = lin.forward(x, act=osm.ACT_SILU, residual=r)
+        bad = [1, M - 2]
+        x[bad[0], 5], x[bad[1], 511] = float("nan"), float("inf")
+        r[2, 7] = float("inf")
+        dirty = lin.forward(x, act=osm.ACT_SILU, residual=r)
+        keep = torch.ones(M, dtype=torch.bool, device="cuda")
+        keep[bad + [2]] = False
+        same(dirty[keep], clean[keep])
+        assert not bool(torch.isfinite(dirty[bad]).all(1).any()) and bool(torch.isinf(dirty[2, 7]))
+        same(dirty[2, :7], clean[2, :7])
+
+
+def test_silu_and_gelu_at_the_ends_of_their_range():
+    v = torch.tensor([0.0, -0.0, 1e-38, -1e-38, 1.0, -1.0, -20.0, -87.0, -88.8, -104.0, 104.0, -1e4, 1e4, 3e38, -3e38],
+                     device="cuda").bfloat16()
+    x = torch.zeros(64, 32, dtype=BF, device="cuda")
+    x[:v.numel(), 0] = v
+    W = torch.eye(32, device="cuda").bfloat16()
+    y = osm.HpLinear(W).forward(x, act=osm.ACT_SILU, dtype=F32)[:v.numel(), 0].double()
+    ref = v.double() * torch.sigmoid(v.double())
+    # relative as derived at check_linear; below 2^-126 results flush to zero
+    assert bool(((y - ref).abs() <= ref.abs() * (8 * U + 4 * U * v.double().abs().clamp_max(200)) + 2.0 ** -119).all())
+    y = osm.HpLinear(W).forward(x, act=osm.ACT_GELU, dtype=F32)[:v.numel() - 1, 0].double()
+    ref = act64(v.double(), osm.ACT_GELU)[:-1]
+    assert bool(((y - ref).abs() <= 5e-7 * ref.abs() + 2e-8 * v[:-1].double().abs()).all())
+
+
+# ------------------------------------------------------------ more than 2^32 values
+
+def room(gib):
+    free, _ = torch.cuda.mem_get_info()
+    if free < gib << 30:
+        pytest.skip(f"needs {gib} GiB of free device memory")
+
+
+def filled(M, D, dtype):
+    """[M][D] values that differ from row to row, without a second buffer of that size."""
+    x = torch.empty(M, D, dtype=dtype, device="cuda")
+    base = rand(gen(1), 4096, D, dtype=dtype)
+    for i in range(0, M, 4096):
+        n = min(4096, M - i)
+        x[i:i + n] = base[:n].roll(i % D, 1)
+    return x
+
+
+def test_norms_past_32_bit_offsets():
+    room(60)
+    M, D = 320_001, 14336
+    x = filled(M, D, BF)
+    at = torch.tensor([0, 1, M // 2, 299_594, M - 2, M - 1], device="cuda")
+    n = osm.Norm(scale=rand(gen(2), D, scale=0.3), shift=rand(gen(3), D))
+    h = osm.norm_modulate(x, n)
+    same(h[at], osm.norm_modulate(x[at], n))
+    out, h = osm.residual_norm(x, h, gate=rand(gen(4), D), pre=n, h=h)
+    few, fh = osm.residual_norm(x[at], osm.norm_modulate(x[at], n), gate=rand(gen(4), D), pre=n)
+    same(out[at], few)
+    same(h[at], fh)
+
+
+def test_norm_quantize_act_past_32_bit_offsets():
+    room(40)
+    M, K = 900_003, 5120
+    plan = make_plan(gen(5), K, 32, 128)
+    x = filled(M, K, BF)
+    n = osm.Norm()
+    a = plan.alloc_packed(M)
+    osm.norm_quantize_act(plan, x, n, *a)
+    at = torch.tensor([0, M // 2, 838_861, M - 1], device="cuda")
+    few = plan.alloc_packed(4)
+    osm.norm_quantize_act(plan, x[at], n, *few)
+    same(a[0].view(M, -1)[at], few[0].view(4, -1))
+    same(a[2].view(M, -1)[at], few[2].view(4, -1))
+
+
+def test_linear_hp_past_32_bit_offsets():
+    room(40)
+    M, K, N = 1_100_003, 64, 4096
+    g = gen(6)
+    x, W = filled(M, K, BF), rand(g, K, N, dtype=BF, scale=0.1)
+    y = filled(M, N, BF)
+    at = torch.tensor([0, 1_048_575, 1_048_577, M - 1], device="cuda")
+    r = y[at]
+    osm.HpLinear(W).forward(x, residual=y, out=y)
+    ref = r.double() + x[at].double() @ W.double()
+    T = x[at].double().abs() @ W.double().abs()
+    e = (K / 16 + 2) * 2 * U * T + U * ref.abs()
+    within(y[at], ref, e + 2.0 ** -8 * (ref.abs() + e))
+
+
 # ------------------------------------------------------------ together
 
 def ffn(g, D, F, k):
