@@ -225,9 +225,8 @@ __global__ void __launch_bounds__(32 * WARPS, MINB) rows_kernel(const __grid_con
     }
 }
 
-// Few rows, very wide ones, or a modulation row for each token: a CTA of as
-// many warps as the row has segments (16 at most) takes one row at a time and
-// reads its coefficients from global memory.
+// Few rows, very wide ones, or a modulation row for each token: a CTA takes one
+// row at a time and reads its coefficients from global memory.
 template <bool F32, bool HAS_Y, int NS, int MINB>
 __global__ void __launch_bounds__(512, MINB) row_kernel(const __grid_constant__ RowParams p) {
     __shared__ float part[2][16 * NS];
@@ -334,7 +333,9 @@ template <bool F32, bool HAS_Y, int NS, int MINB>
 int launch_single(const RowParams& p, cudaStream_t st) {
     static Setup su;
     auto kern = row_kernel<F32, HAS_Y, NS, MINB>;
-    const int threads = 32 * static_cast<int>(std::min<int64_t>(16, ceil_div(p.D, norm::SEG)));
+    // a warp per segment for few rows; for many, as many segments as a warp can hold
+    const int64_t nseg = ceil_div(p.D, norm::SEG);
+    const int threads = 32 * static_cast<int>(std::min<int64_t>(16, p.M < 4 * 148 ? nseg : ceil_div(nseg, NS)));
     int ctas = 0;
     OSM_TRY(prepare(su, reinterpret_cast<const void*>(kern), threads, 0, &ctas));
     return launch(kern, std::min<uint32_t>(p.M, ctas), threads, 0, st, p);
@@ -342,10 +343,11 @@ int launch_single(const RowParams& p, cudaStream_t st) {
 
 template <bool F32, bool HAS_Y>
 int launch_width(const RowParams& p, cudaStream_t st) {
-    // Tiles pay once a CTA has about 16 rows (M from about 2400 rows on) and
-    // runs long enough to lay out their coefficients once.
-    // The coefficients of 14336 columns (both tables) fill shared memory.
-    const bool tiles = p.M >= 148 * 16 && p.share >= 64 && p.D <= 14336;
+    // Tiles pay from two rows per SM on, while a run's coefficients serve a few
+    // rows (5120 columns in us, a CTA per row against tiles: 100 rows 7.7 and 8.8,
+    // 300 rows 11.1 and 9.3, 3000 rows 38.7 and 19.8). The coefficients of 14336
+    // columns (both tables) fill shared memory.
+    const bool tiles = p.M >= 2 * 148 && p.share >= 8 && p.D <= 14336;
     if (!tiles) {
         if (p.D <= 8192) return launch_single<F32, HAS_Y, 2, 2>(p, st);
         if (p.D <= 16384) return launch_single<F32, HAS_Y, 4, F32 ? 1 : 2>(p, st);

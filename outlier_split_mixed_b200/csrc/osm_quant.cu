@@ -1637,9 +1637,11 @@ int launch_norm_quantize(const osm_plan* pl, const void* X, int x_dtype, int64_t
     const int mode = pl->fmt == OSM_FMT_NVFP4 ? QA_NV : (pl->hp_fp16 ? QA_MX_F16 : QA_MX);
     const int nseg = static_cast<int>(ceil_div(pl->K, norm::SEG));
     const int64_t run = spec->scale || spec->shift ? (M < spec->mod_rows ? M : spec->mod_rows) : M;
-    // Many rows: teams of warps (see norm_quantize_rows_kernel). Below about
-    // eight rows per SM its tables cost more than they save.
-    if (pl->K <= 5120 && run >= 64 && M >= 148 * 8) {
+    // Teams of warps (norm_quantize_rows_kernel) while a row pair fits their
+    // registers, unless the tables would have to be laid out anew for every few
+    // rows of many (5120 columns in us, one row per CTA against teams: 1 row 17.5
+    // and 11.5, 1000 rows 29.2 and 16.8, 4000 rows in runs of 16 71 and 41).
+    if (pl->K <= 5120 && (run >= 8 || M <= 148)) {
         if (pl->K <= 1024) return launch_norm_quantize_rows<2, 2, 2>(p, mode, s, X, f32, M, run, st);
         return launch_norm_quantize_rows<4, 5, 1>(p, mode, s, X, f32, M, run, st);
     }
