@@ -359,10 +359,12 @@ int launch_width(const RowParams& p, cudaStream_t st) {
     // barriers and shuffles cost more than the latency that they hide. 32760 x 5120
     // BF16 in us, norm_modulate: 1 warp of 20 segments and 16 warps per CTA 127.5, 2
     // x 10 122.0, 4 x 5 and 28 warps 119.2; residual_norm: 2 x 10 and 16 warps 242.1,
-    // 4 x 5 and 24 warps 237.2, 28 warps 252 (spills).
+    // 4 x 5 and 24 warps 237.2, 28 warps 252 (spills). 60000 x 2048 FP32 with a
+    // post-norm: 1 x 8 265, 2 x 4 260, 4 x 2 238.
     if (p.D <= 512) return launch_tiles<F32, HAS_Y, 1, 2, 16, 2>(p, st);
     if (p.D <= 2048) {
-        if constexpr (HAS_Y) return launch_tiles<F32, HAS_Y, 2, 4, 24, 1>(p, st);
+        if constexpr (HAS_Y && F32) return launch_tiles<F32, HAS_Y, 4, 2, 24, 1>(p, st);
+        else if constexpr (HAS_Y) return launch_tiles<F32, HAS_Y, 2, 4, 20, 1>(p, st);
         else return launch_tiles<F32, HAS_Y, 2, 4, 16, 2>(p, st);
     }
     if (p.D <= 5120) {
