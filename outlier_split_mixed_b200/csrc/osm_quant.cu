@@ -1149,89 +1149,77 @@ __global__ void __launch_bounds__(QA_THREADS) norm_quantize_kernel(QuantParams p
     }
 }
 
-// The form for many rows of at most 5120 columns. Issue slots bound it (the
-// rows are read once), so a row pair stays with one team of two warps and the
-// team meets only four times per pair; the other teams of the CTA fill in:
+// Encode half a staged block (16 positions) of both rows of a pair (paired
+// staging, see quantize_act_pair_kernel): the words are read once and stay in
+// registers; the two lanes of an MXFP4 block exchange their maxima. Called by
+// whole warps, lanes 2i and 2i + 1 on the halves of one block; `on` is false
+// past the last block.
+template <int MODE>
+__device__ __forceinline__ void encode_pair_half(const QuantParams& p, uint32_t sbuf, int t0, int rows, int hb, bool on) {
+    const int b = hb >> 1, half = hb & 1;
+    const uint32_t src = sbuf + b * IP_BLOCK + half * 64;
+    const uint4 v0 = ptx::ld_shared_v4(src), v1 = ptx::ld_shared_v4(src + 16), v2 = ptx::ld_shared_v4(src + 32),
+                v3 = ptx::ld_shared_v4(src + 48);
+    using mx::bf16x2_absmax;
+    uint32_t m = bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(v0.x, v0.y), bf16x2_absmax(v0.z, v0.w)),
+                                             bf16x2_absmax(bf16x2_absmax(v1.x, v1.y), bf16x2_absmax(v1.z, v1.w))),
+                               bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(v2.x, v2.y), bf16x2_absmax(v2.z, v2.w)),
+                                             bf16x2_absmax(bf16x2_absmax(v3.x, v3.y), bf16x2_absmax(v3.z, v3.w))));
+    if constexpr (MODE != QA_NV) m = bf16x2_absmax(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    const uint32_t m0 = m & 0x7FFFu, m1 = (m >> 16) & 0x7FFFu;
+    if (!on) return;
+    float f0, f1;  // element multipliers of the two rows
+    if constexpr (MODE == QA_NV) {
+        const uint32_t s = mx::nv_block_scales(m0, m1, p.nv_k, p.nv_p2g, &f0, &f1);
+        p.scales[sf_offset(t0, hb, p.katoms)] = static_cast<uint8_t>(s);
+        if (rows == 2) p.scales[sf_offset(t0 + 1, hb, p.katoms)] = static_cast<uint8_t>(s >> 8);
+    } else {
+        const bool real = b * 32 < p.Kb;
+        const int X0 = mx::bf16_block_exponent(m0, &f0), X1 = mx::bf16_block_exponent(m1, &f1);
+        // the block's scale bytes: row 0 by the first lane, row 1 by the second
+        if (half < rows) p.scales[sf_offset(t0 + half, b, p.katoms)] = static_cast<uint8_t>(real ? (half ? X1 : X0) + 127 : 0);
+    }
+    const uint32_t w[16] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w, v2.x, v2.y, v2.z, v2.w, v3.x, v3.y, v3.z, v3.w};
+    const size_t cstride = static_cast<size_t>(p.Kbp >> 1);
+    uint8_t* codes = p.codes + static_cast<size_t>(t0) * cstride + hb * 8;
+    *reinterpret_cast<uint2*>(codes) = make_uint2(encode8_halves<false>(w, f0), encode8_halves<false>(w + 8, f0));
+    if (rows == 2)
+        *reinterpret_cast<uint2*>(codes + cstride) = make_uint2(encode8_halves<true>(w, f1), encode8_halves<true>(w + 8, f1));
+}
+
+// The form for rows of at most 5120 columns. Issue slots bound it (each row is
+// read once), so a pair of rows stays with one team of W warps, which meets only
+// four times per pair; the other teams of the CTA fill in:
 //   each lane holds chunks of 8 columns of both rows in registers (one 128-bit
 //   load each) for the statistics, as in osm_norm.cu;
 //   it normalises, modulates, rounds, smooths and rounds them -- coefficients
 //   and inv_s of the run in shared memory, read once for both rows -- and
-//   stores the 16-bit values at their routed places in the team's staged rows;
-//   then the team encodes the staged rows, a 32-block per lane at a time.
-// Staged rows are plain: bulk position p at byte 2p, the slots behind Kbp. A
-// lane stores its chunk's four words starting from the one that makes the
-// banks of lanes 8 apart differ (lanes next to one another differ by
-// themselves); the start is laid out in the route table, from the chunk's
-// address. In the encoding, lanes two blocks apart start their four 128-bit
-// reads from different units, which makes them conflict-free; the four code
-// words are put in order afterwards.
-// Two teams' worth of FP32 rows would not fit the registers: one row per team.
-
-template <int W, int NS>
+//   stores each column's two values as one word at its routed place in the
+//   team's paired staging;
+//   then the team encodes the staged pair, half a block of both rows per lane.
+// 32760 x 5120 BF16: 161 us (2.6 TB/s of reads and writes; the two calls that it
+// stands for take 119 + 93 us), at 116 million warp instructions, 0.65 of the issue
+// slots. On the way here: one row per CTA 415 us; a pair of rows per CTA of 20
+// warps 315 (each warp repeats the joins and waits at four block barriers); teams
+// of two warps with rows staged apart 210, with 16-bit stores ordered by bank 199;
+// four warps and 24 warps per SM 166; paired words 161.
+template <int W, int NS, int TEAMS_>
 struct NormQuantShape {
-    static constexpr int COLS = W * NS * norm::SEG;            // widest row
-    static constexpr int STRIDE = 2 * (COLS + 128 + 64);       // bytes of one staged row (Kbp + kp <= K + 192)
-    static constexpr int TEAMS = COLS > 1024 ? 24 / W : 16 / W;
+    static constexpr int TEAMS = TEAMS_;
     static constexpr int THREADS = 32 * W * TEAMS;
-    static constexpr int smem(int K, int R) {
-        return TEAMS * (R * STRIDE + 2 * R * W * NS * 4) + (K / norm::CHUNK) * 7 * 16;
+    // [TEAMS] staged pairs, [TEAMS][2][2][W * NS] segment totals, the tables
+    __host__ __device__ static constexpr int stage(int nb, int kp) { return (qa_ip_bytes(nb, kp) + 15) & ~15; }
+    static int smem(int K, int nb, int kp) {
+        return TEAMS * (stage(nb, kp) + 4 * W * NS * 4) + (K / norm::CHUNK) * 8 * 16;
     }
 };
 
-// Words 0..3 one place down (by1) and two (by2), around the end.
-__device__ __forceinline__ void rotate_words(uint32_t (&w)[4], bool by1, bool by2) {
-    const uint32_t x0 = by1 ? w[1] : w[0], x1 = by1 ? w[2] : w[1], x2 = by1 ? w[3] : w[2], x3 = by1 ? w[0] : w[3];
-    w[0] = by2 ? x2 : x0;
-    w[1] = by2 ? x3 : x1;
-    w[2] = by2 ? x0 : x2;
-    w[3] = by2 ? x1 : x3;
-}
-
-// One 32-block of row t from its 64 staged bytes at `src`: its maxima,
-// scale(s) and codes, with the four 16-byte units read from unit (b / 2) % 4 on, around the end.
-template <int MODE>
-__device__ __forceinline__ void encode_turned_block(const QuantParams& p, int t, int b, uint32_t src) {
-    const int turn = b >> 1;
-    uint4 q[4];
-    uint32_t m[4];  // packed maxima of the units, in the order read
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        q[i] = ptx::ld_shared_v4(src + ((i + turn) & 3) * 16);
-        m[i] = mx::bf16x2_absmax(mx::bf16x2_absmax(q[i].x, q[i].y), mx::bf16x2_absmax(q[i].z, q[i].w));
-    }
-    // unit u was read (u - turn)-th: turning 4 - turn places more puts them in order
-    const bool by1 = turn & 1, by2 = ((turn >> 1) ^ turn) & 1;  // bits of (-turn) & 3
-    uint32_t code[4];
-    uint8_t* codes = p.codes + static_cast<size_t>(t) * (p.Kbp >> 1) + b * 16;
-    if constexpr (MODE == QA_NV) {
-        uint32_t o[4] = {m[0], m[1], m[2], m[3]};
-        rotate_words(o, by1, by2);
-        const uint32_t lo = mx::bf16x2_absmax(o[0], o[1]), hi = mx::bf16x2_absmax(o[2], o[3]);
-        float r_lo, r_hi;
-        const uint32_t s2 = mx::nv_block_scales(max(lo & 0x7FFFu, (lo >> 16) & 0x7FFFu), max(hi & 0x7FFFu, (hi >> 16) & 0x7FFFu),
-                                                p.nv_k, p.nv_p2g, &r_lo, &r_hi);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) code[i] = encode8_words(q[i], ((i + turn) & 2) ? r_hi : r_lo);
-        *reinterpret_cast<uint16_t*>(p.scales + sf_offset(t, 2 * b, p.katoms)) = static_cast<uint16_t>(s2);
-    } else {
-        const uint32_t mm = mx::bf16x2_absmax(mx::bf16x2_absmax(m[0], m[1]), mx::bf16x2_absmax(m[2], m[3]));
-        float inv;
-        const int X = mx::bf16_block_exponent(max(mm & 0x7FFFu, (mm >> 16) & 0x7FFFu), &inv);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) code[i] = encode8_words(q[i], inv);
-        p.scales[sf_offset(t, b, p.katoms)] = static_cast<uint8_t>(b * 32 < p.Kb ? X + 127 : 0);
-    }
-    rotate_words(code, by1, by2);
-    *reinterpret_cast<uint4*>(codes) = make_uint4(code[0], code[1], code[2], code[3]);
-}
-
-template <int MODE, bool F32, int W, int NS, int MINB>
-__global__ void __launch_bounds__(NormQuantShape<W, NS>::THREADS, MINB)
+template <int MODE, bool F32, int W, int NS, int TEAMS, int MINB>
+__global__ void __launch_bounds__(NormQuantShape<W, NS, TEAMS>::THREADS, MINB)
     norm_quantize_rows_kernel(QuantParams p, norm::Spec s, const void* X, uint32_t share, uint32_t tile_rows,
                               uint32_t tiles_per_run, uint32_t tiles) {
-    using Shape = NormQuantShape<W, NS>;
+    using Shape = NormQuantShape<W, NS, TEAMS>;
     constexpr bool HPF = MODE == QA_MX_F16;
-    constexpr int R = F32 ? 1 : 2;
     constexpr int XQ = F32 ? 2 : 1;
     ptx::grid_dep_wait();    // launched while the kernel before it finishes
     ptx::grid_dep_launch();  // the dual_gemm that follows may start its prologue
@@ -1240,42 +1228,29 @@ __global__ void __launch_bounds__(NormQuantShape<W, NS>::THREADS, MINB)
     const int nb = p.Kbp >> 5, nchunk = p.K / norm::CHUNK, nseg = (p.K + norm::SEG - 1) / norm::SEG, hv = p.kp >> 3;
     const bool center = s.kind == OSM_NORM_LAYER;
     const float inv_d = __frcp_rn(static_cast<float>(p.K));
-    // [TEAMS][R] staged rows, [TEAMS][2][R][W * NS] segment totals, the tables
-    const uint32_t stage = ptx::smem_u32(smem) + team * R * Shape::STRIDE;
-    float* part = reinterpret_cast<float*>(smem + Shape::TEAMS * R * Shape::STRIDE) + team * 2 * R * W * NS;
-    uint4* table = reinterpret_cast<uint4*>(smem + Shape::TEAMS * (R * Shape::STRIDE + 2 * R * W * NS * 4));
-    // words of chunk c: a, a, b, b (table[i * nchunk + c], i = 0..3), inv_s (4, 5), routes (6: staged bytes of the
-    // two columns of the word that is stored i-th; bits 14 and 15 of the first hold the number of that word)
+    const int stage_bytes = Shape::stage(nb, p.kp);
+    const uint32_t stage = ptx::smem_u32(smem) + team * stage_bytes;
+    float* part = reinterpret_cast<float*>(smem + TEAMS * stage_bytes) + team * 4 * W * NS;
+    uint4* table = reinterpret_cast<uint4*>(smem + TEAMS * (stage_bytes + 4 * W * NS * 4));
+    // words of chunk c: a, a, b, b (table[i * nchunk + c], i = 0..3), inv_s (4, 5), staged bytes of its columns (6, 7)
 
-    // staged byte of channel position `off` (an offset of the plan's route table)
-    auto staged = [&](int off) -> uint32_t {
-        if (off >= nb * QA_BLOCK_BYTES) return p.Kbp * 2 + (off - nb * QA_BLOCK_BYTES);
+    auto staged = [&](int off) -> uint32_t {  // of an offset of the plan's route table
+        if (off >= nb * QA_BLOCK_BYTES) return nb * IP_BLOCK + ((off - nb * QA_BLOCK_BYTES) >> 1) * 4;
         const int b = off / QA_BLOCK_BYTES;
-        return b * 64 + (off - b * QA_BLOCK_BYTES);
+        return b * IP_BLOCK + ((off - b * QA_BLOCK_BYTES) >> 1) * 4;
     };
-    static_assert(Shape::STRIDE <= 1 << 14, "bits 14 and 15 of a staged byte are free");
-    for (int c = tid; c < nchunk; c += Shape::THREADS) {
-        const int2* rt = reinterpret_cast<const int2*>(p.route) + 4 * c;
-        uint32_t word[4];
-        const uint32_t start = (((c & 31) >> 3) - (staged(__ldg(rt).x) >> 2)) & 3;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int2 dv = __ldg(rt + ((i + start) & 3));
-            word[i] = staged(dv.x) | staged(dv.y) << 16;
-        }
-        word[0] |= start << 14;
-        table[6 * nchunk + c] = make_uint4(word[0], word[1], word[2], word[3]);
-        table[4 * nchunk + c] = __ldg(reinterpret_cast<const uint4*>(p.inv_s) + 2 * c);
-        table[5 * nchunk + c] = __ldg(reinterpret_cast<const uint4*>(p.inv_s) + 2 * c + 1);
+    for (int i = tid; i < 2 * nchunk; i += Shape::THREADS) {
+        const int half = i >= nchunk, c = i - half * nchunk;
+        const int4 rt = __ldg(reinterpret_cast<const int4*>(p.route) + 2 * c + half);
+        table[(6 + half) * nchunk + c] = make_uint4(staged(rt.x), staged(rt.y), staged(rt.z), staged(rt.w));
+        table[(4 + half) * nchunk + c] = __ldg(reinterpret_cast<const uint4*>(p.inv_s) + 2 * c + half);
     }
-    // padding positions (bulk [Kb, Kbp), slots [k, kp)) of the staged rows are zeroed once
+    // padding positions (bulk [Kb, Kbp), slots [k, kp)) of the staged pair are zeroed once
     {
         const int npb = p.Kbp - p.Kb, npad = npb + (p.kp - p.k);
-        for (int i = tt; i < R * npad; i += 32 * W) {
-            const int r = i / npad, c = i - r * npad;
+        for (int c = tt; c < npad; c += 32 * W) {
             const int pos = p.Kb + c;
-            const uint32_t at = c < npb ? pos * 2 : p.Kbp * 2 + (p.k + c - npb) * 2;
-            ptx::st_shared_u16(stage + r * Shape::STRIDE + at, 0);
+            ptx::st_shared_u32(stage + (c < npb ? (pos >> 5) * IP_BLOCK + (pos & 31) * 4 : nb * IP_BLOCK + (p.k + c - npb) * 4), 0u);
         }
     }
     auto team_sync = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(32 * W) : "memory"); };
@@ -1299,14 +1274,14 @@ __global__ void __launch_bounds__(NormQuantShape<W, NS>::THREADS, MINB)
             }
             __syncthreads();
         }
-        for (uint32_t row = row0 + R * team; row < end; row += R * Shape::TEAMS) {
-            const int rows = R == 1 ? 1 : static_cast<int>(min(2u, end - row));
-            uint4 xq[R][NS][XQ];
+        for (uint32_t row = row0 + 2 * team; row < end; row += 2 * TEAMS) {
+            const int rows = static_cast<int>(min(2u, end - row));
+            uint4 xq[2][NS][XQ];
 #pragma unroll
             for (int t = 0; t < NS; ++t) {
                 const int c = (j + t * W) * 32 + lane;
 #pragma unroll
-                for (int r = 0; r < R; ++r)
+                for (int r = 0; r < 2; ++r)
 #pragma unroll
                     for (int q = 0; q < XQ; ++q)
                         xq[r][t][q] = c < nchunk && r < rows
@@ -1319,18 +1294,17 @@ __global__ void __launch_bounds__(NormQuantShape<W, NS>::THREADS, MINB)
                 else norm::unpack(xq[r][t][0], v);
             };
             // totals over each row of one value per chunk
-            float value[R][NS];
+            float value[2][NS];
             auto totals = [&](float* at) -> float2 {
 #pragma unroll
-                for (int r = 0; r < R; ++r) norm::warp_totals<NS>(value[r], lane, at + r * W * NS + j, W);
+                for (int r = 0; r < 2; ++r) norm::warp_totals<NS>(value[r], lane, at + r * W * NS + j, W);
                 team_sync();
-                if (R == 2) return norm::join_totals2(at, at + W * NS, nseg, lane);
-                return make_float2(norm::join_total<W * NS>(at, nseg, lane), 0.0f);
+                return norm::join_totals2(at, at + W * NS, nseg, lane);
             };
             float2 mean = make_float2(0.0f, 0.0f);
             if (center) {
 #pragma unroll
-                for (int r = 0; r < R; ++r)
+                for (int r = 0; r < 2; ++r)
 #pragma unroll
                     for (int t = 0; t < NS; ++t) {
                         float2 v[4];
@@ -1341,14 +1315,14 @@ __global__ void __launch_bounds__(NormQuantShape<W, NS>::THREADS, MINB)
                 mean = __fmul2_rn(mean, make_float2(inv_d, inv_d));
             }
 #pragma unroll
-            for (int r = 0; r < R; ++r)
+            for (int r = 0; r < 2; ++r)
 #pragma unroll
                 for (int t = 0; t < NS; ++t) {
                     float2 v[4];
                     x_of(r, t, v);
                     value[r][t] = (j + t * W) * 32 + lane < nchunk ? norm::chunk_m2(v, r ? mean.y : mean.x) : 0.0f;
                 }
-            const float2 m2 = totals(part + R * W * NS);
+            const float2 m2 = totals(part + 2 * W * NS);
             const float2 st[2] = {make_float2(mean.x, norm::inverse_deviation(m2.x, inv_d, s.eps)),
                                   make_float2(mean.y, norm::inverse_deviation(m2.y, inv_d, s.eps))};
             // (the barrier of the totals also comes after the encoding of the team's last rows)
@@ -1358,54 +1332,40 @@ __global__ void __launch_bounds__(NormQuantShape<W, NS>::THREADS, MINB)
                 if (c >= nchunk) continue;
                 const uint4* at = table + c;
                 const uint4 a0 = at[0], a1 = at[nchunk], b0 = at[2 * nchunk], b1 = at[3 * nchunk], s0 = at[4 * nchunk],
-                            s1 = at[5 * nchunk], rt = at[6 * nchunk];
+                            s1 = at[5 * nchunk], r0 = at[6 * nchunk], r1 = at[7 * nchunk];
                 auto pair = [](uint32_t x, uint32_t y) { return make_float2(__uint_as_float(x), __uint_as_float(y)); };
                 const float2 ca[4] = {pair(a0.x, a0.y), pair(a0.z, a0.w), pair(a1.x, a1.y), pair(a1.z, a1.w)};
                 const float2 cb[4] = {pair(b0.x, b0.y), pair(b0.z, b0.w), pair(b1.x, b1.y), pair(b1.z, b1.w)};
                 const float2 cs[4] = {pair(s0.x, s0.y), pair(s0.z, s0.w), pair(s1.x, s1.y), pair(s1.z, s1.w)};
-                const uint32_t to[4] = {rt.x & ~0xC000u, rt.y, rt.z, rt.w};
-                const bool by1 = rt.x & 0x4000u, by2 = rt.x & 0x8000u;
+                const uint32_t to[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+                float2 x0[4], x1[4];
+                x_of(0, t, x0);
+                x_of(1, t, x1);
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    float2 v[4];
-                    x_of(r, t, v);
-                    uint32_t w[4], u[4];  // BF16, and binary16 for the slots of an FP16 outlier branch
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        w[i] = norm_smooth2<false>(v[i], st[r], ca[i], cb[i], cs[i], 0u);
-                        if constexpr (HPF) u[i] = norm_smooth2<true>(v[i], st[r], ca[i], cb[i], cs[i], 0xFFFFFFFFu);
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t w0 = norm_smooth2<false>(x0[i], st[0], ca[i], cb[i], cs[i], 0u);
+                    const uint32_t w1 = norm_smooth2<false>(x1[i], st[1], ca[i], cb[i], cs[i], 0u);
+                    uint32_t lo = __byte_perm(w0, w1, 0x5410), hi = __byte_perm(w0, w1, 0x7632);
+                    if constexpr (HPF) {  // the slots of an FP16 outlier branch: the same products in binary16
+                        const uint32_t u0 = norm_smooth2<true>(x0[i], st[0], ca[i], cb[i], cs[i], 0xFFFFFFFFu);
+                        const uint32_t u1 = norm_smooth2<true>(x1[i], st[1], ca[i], cb[i], cs[i], 0xFFFFFFFFu);
+                        const uint32_t slots = nb * IP_BLOCK;
+                        if (to[2 * i] >= slots) lo = __byte_perm(u0, u1, 0x5410);
+                        if (to[2 * i + 1] >= slots) hi = __byte_perm(u0, u1, 0x7632);
                     }
-                    rotate_words(w, by1, by2);
-                    if constexpr (HPF) {
-                        rotate_words(u, by1, by2);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t mask = ((to[i] & 0xFFFFu) >= p.Kbp * 2u ? 0x0000FFFFu : 0u) |
-                                                  ((to[i] >> 16) >= p.Kbp * 2u ? 0xFFFF0000u : 0u);
-                            w[i] = (w[i] & ~mask) | (u[i] & mask);
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        ptx::st_shared_u16(stage + (to[i] & 0xFFFFu) + r * Shape::STRIDE, w[i]);
-                        ptx::st_shared_u16(stage + (to[i] >> 16) + r * Shape::STRIDE, w[i] >> 16);
-                    }
+                    ptx::st_shared_u32(stage + to[2 * i], lo);
+                    ptx::st_shared_u32(stage + to[2 * i + 1], hi);
                 }
             }
-            team_sync();  // staged rows complete
+            team_sync();  // staged pair complete
+            const int nhb = 2 * nb, t0 = static_cast<int>(row);
 #pragma unroll 1
-            for (int i = tt; i < rows * nb; i += 32 * W) {
-                const int r = i >= nb, b = i - r * nb, row_r = static_cast<int>(row) + r;
-                const uint32_t src = stage + r * Shape::STRIDE + b * 64;
-                encode_turned_block<MODE>(p, row_r, b, src);
+            for (int b0 = 32 * j; b0 < nhb; b0 += 32 * W) {
+                const int hb = b0 + lane;
+                encode_pair_half<MODE>(p, stage, t0, rows, min(hb, nhb - 2 + (hb & 1)), hb < nhb);
             }
 #pragma unroll 1
-            for (int i = 32 * W - 1 - tt; i < rows * hv; i += 32 * W) {
-                const int r = i >= hv, c = i - r * hv;
-                uint4 v = ptx::ld_shared_v4(stage + r * Shape::STRIDE + p.Kbp * 2 + c * 16);
-                if constexpr (MODE == QA_NV) v = mx::scale_bf16x8(v, p.hp_scale);
-                *reinterpret_cast<uint4*>(p.hp + static_cast<size_t>(row + r) * p.kp + c * 8) = v;
-            }
+            for (int c = 32 * W - 1 - tt; c < hv; c += 32 * W) copy_pair_slots<MODE>(p, stage, nb, t0, rows, c);
         }
         if (row0 < static_cast<uint32_t>(p.M) && end == static_cast<uint32_t>(p.M)) zero_padding_scale_rows(p);
     }
@@ -1603,19 +1563,16 @@ static int launch_dependent(K kern, unsigned grid, unsigned threads, size_t smem
     return check_cuda(cudaLaunchKernelEx(&cfg, kern, args...), "norm_quantize_act launch");
 }
 
-template <int W, int NS, int MINB>
-static int launch_norm_quantize_rows(const QuantParams& p, int mode, const norm::Spec& s, const void* X, bool f32, int64_t M,
+template <bool F32, int W, int NS, int TEAMS, int MINB>
+static int launch_norm_quantize_rows(const QuantParams& p, int mode, const norm::Spec& s, const void* X, int64_t M,
                                      int64_t run, cudaStream_t st) {
-    auto pick = [&](auto f) {
-        constexpr bool F = decltype(f)::value;
-        return mode == QA_NV ? norm_quantize_rows_kernel<QA_NV, F, W, NS, MINB>
-                             : (mode == QA_MX_F16 ? norm_quantize_rows_kernel<QA_MX_F16, F, W, NS, MINB>
-                                                  : norm_quantize_rows_kernel<QA_MX, F, W, NS, MINB>);
-    };
-    auto kern = f32 ? pick(std::true_type{}) : pick(std::false_type{});
-    const size_t smem = NormQuantShape<W, NS>::smem(p.K, f32 ? 1 : 2);
+    using Shape = NormQuantShape<W, NS, TEAMS>;
+    auto kern = mode == QA_NV ? norm_quantize_rows_kernel<QA_NV, F32, W, NS, TEAMS, MINB>
+                              : (mode == QA_MX_F16 ? norm_quantize_rows_kernel<QA_MX_F16, F32, W, NS, TEAMS, MINB>
+                                                   : norm_quantize_rows_kernel<QA_MX, F32, W, NS, TEAMS, MINB>);
+    const size_t smem = Shape::smem(p.K, p.Kbp >> 5, p.kp);
     int per_sm = 0, sms = 0;
-    int rc = prepare_kernel(reinterpret_cast<const void*>(kern), NormQuantShape<W, NS>::THREADS, smem, &per_sm, &sms);
+    int rc = prepare_kernel(reinterpret_cast<const void*>(kern), Shape::THREADS, smem, &per_sm, &sms);
     if (rc) return rc;
     if (per_sm < 1) return fail(OSM_ERR_UNSUPPORTED, "norm_quantize_act: no CTA fits (K = %d)", p.K);
     // one tile per CTA: each run is cut into its part of them
@@ -1623,7 +1580,7 @@ static int launch_norm_quantize_rows(const QuantParams& p, int mode, const norm:
     const int64_t cuts = ctas * run / M > 1 ? ctas * run / M : 1;
     const int64_t tile_rows = ceil_div(run, cuts), per_run = ceil_div(run, tile_rows);
     const int64_t tiles = ceil_div(M, run) * per_run;
-    return launch_dependent(kern, static_cast<unsigned>(tiles < ctas ? tiles : ctas), NormQuantShape<W, NS>::THREADS, smem,
+    return launch_dependent(kern, static_cast<unsigned>(tiles < ctas ? tiles : ctas), Shape::THREADS, smem,
                             st, p, s, X, static_cast<uint32_t>(run), static_cast<uint32_t>(tile_rows),
                             static_cast<uint32_t>(per_run), static_cast<uint32_t>(tiles));
 }
@@ -1642,8 +1599,11 @@ int launch_norm_quantize(const osm_plan* pl, const void* X, int x_dtype, int64_t
     // rows of many (5120 columns in us, one row per CTA against teams: 1 row 17.5
     // and 11.5, 1000 rows 29.2 and 16.8, 4000 rows in runs of 16 71 and 41).
     if (pl->K <= 5120 && (run >= 8 || M <= 148)) {
-        if (pl->K <= 1024) return launch_norm_quantize_rows<2, 2, 2>(p, mode, s, X, f32, M, run, st);
-        return launch_norm_quantize_rows<4, 5, 1>(p, mode, s, X, f32, M, run, st);
+        if (pl->K <= 1024)
+            return f32 ? launch_norm_quantize_rows<true, 2, 2, 8, 2>(p, mode, s, X, M, run, st)
+                       : launch_norm_quantize_rows<false, 2, 2, 8, 2>(p, mode, s, X, M, run, st);
+        return f32 ? launch_norm_quantize_rows<true, 4, 5, 4, 1>(p, mode, s, X, M, run, st)
+                   : launch_norm_quantize_rows<false, 4, 5, 6, 1>(p, mode, s, X, M, run, st);
     }
     const size_t smem = ((2 * nseg * 4 + 15) & ~15) + qa_row_stride(static_cast<int>(pl->Kbp / 32), static_cast<int>(pl->kp));
     auto pick = [&](auto f) {
