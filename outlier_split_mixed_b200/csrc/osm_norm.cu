@@ -357,10 +357,11 @@ int launch_width(const RowParams& p, cudaStream_t st) {
     // of NS segments: 4 registers for BF16, 8 for FP32, 4 more for y), measured at
     // 2048 and 5120 columns: fewer registers and more warps until the totals'
     // barriers and shuffles cost more than the latency that they hide. 32760 x 5120
-    // BF16 in us, norm_modulate: 1 warp of 20 segments and 16 warps per CTA 127.5, 2
-    // x 10 122.0, 4 x 5 and 28 warps 119.2; residual_norm: 2 x 10 and 16 warps 242.1,
-    // 4 x 5 and 24 warps 237.2, 28 warps 252 (spills). 60000 x 2048 FP32 with a
-    // post-norm: 1 x 8 265, 2 x 4 260, 4 x 2 238.
+    // BF16, back to back, in us: norm_modulate with 1 warp of 20 segments and 16
+    // warps per CTA 123.5, 2 x 10 and 16 warps 125, 20 warps 121.0 (85 % of the
+    // measured copy rate), 4 x 5 and 24 warps 129, 28 warps 125.6; residual_norm with
+    // any of them 227 (90 %). 60000 x 2048 FP32 with a post-norm: 1 x 8 265, 2 x 4
+    // 260, 4 x 2 238.
     if (p.D <= 512) return launch_tiles<F32, HAS_Y, 1, 2, 16, 2>(p, st);
     if (p.D <= 2048) {
         if constexpr (HAS_Y && F32) return launch_tiles<F32, HAS_Y, 4, 2, 24, 1>(p, st);
@@ -369,7 +370,7 @@ int launch_width(const RowParams& p, cudaStream_t st) {
     }
     if (p.D <= 5120) {
         if constexpr (F32) return launch_tiles<F32, HAS_Y, HAS_Y ? 4 : 2, HAS_Y ? 5 : 10, 16, 1>(p, st);
-        else return launch_tiles<F32, HAS_Y, 4, 5, HAS_Y ? 24 : 28, 1>(p, st);
+        else return launch_tiles<F32, HAS_Y, HAS_Y ? 4 : 2, HAS_Y ? 5 : 10, HAS_Y ? 24 : 20, 1>(p, st);
     }
     constexpr int V = F32 || HAS_Y ? 4 : 2;
     if (p.D <= 8192) return launch_tiles<F32, HAS_Y, V, 32 / V, 16, 1>(p, st);
