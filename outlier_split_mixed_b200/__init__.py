@@ -852,7 +852,8 @@ class QuantLinear:
     """A packed layer: plan + resident packed weights. `forward(X)` runs
     quantize_act and dual_gemm on the current stream; with `norm` the rows
     are normalised on the way (norm_quantize_act), with `residual` the
-    product is gated and added to it (dual_gemm_residual)."""
+    product is gated and added to it and has its type, whatever epi says
+    (dual_gemm_residual)."""
 
     def __init__(self, plan: Plan, W, bias=None, device="cuda"):
         self.plan = plan
