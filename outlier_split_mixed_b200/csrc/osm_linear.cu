@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(SK_THREADS) skinny_kernel(const __grid_constan
         }
     }
     float4 bias = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // of the channels that this lane finishes
-    if (p.end.bias && n0 + 4 * lane < p.end.N) bias = __ldg(reinterpret_cast<const float4*>(p.end.bias + n0 + 4 * lane));
+    if (p.end.bias && n0 + 4 * lane < p.end.N) bias = ptx::ld_f4(p.end.bias + n0 + 4 * lane);
     // FP32: a lane adds up its channel's chunk sums for all tokens
     float sum[F32 ? SUMS : 1];
     if constexpr (F32) {
@@ -541,9 +541,9 @@ __global__ void __launch_bounds__(SK_THREADS) skinny_kernel(const __grid_constan
                 const uint32_t off = ring_u32 + (t * ROWS + 4 * lane) * 4;
                 v[u] = splits == 1 ? *reinterpret_cast<const float4*>(part + t * ROWS + 4 * lane) : ld_cluster_f4(ptx::mapa(off, 0));
                 if (p.end.onto.gate)
-                    g[u] = __ldg(reinterpret_cast<const float4*>(
+                    g[u] = ptx::ld_f4(
                         p.end.onto.gate +
-                        (static_cast<uint32_t>(m0 + t) / static_cast<uint32_t>(p.end.onto.gate_rows)) * p.end.onto.gate_stride + n));
+                        (static_cast<uint32_t>(m0 + t) / static_cast<uint32_t>(p.end.onto.gate_rows)) * p.end.onto.gate_stride + n);
                 if (p.end.onto.r) w[u] = static_cast<const Quad*>(p.end.onto.r)[((m0 + t) * p.end.N + n) >> 2];
             }
             for (int s = 1; s < splits; ++s) {

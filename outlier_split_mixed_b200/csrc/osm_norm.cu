@@ -37,26 +37,16 @@ struct RowParams {
     int D;
 };
 
-// Loads of the rows: each byte is read once, so they bypass L1 (which serves
-// the coefficients).
-__device__ __forceinline__ uint4 ld_row(const uint4* p) {
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
-
 // h = n a + b of the pre-norm, and (y or its norm) a + b of the gated sum:
 // alpha, gate and the post-norm's affine part in one pair.
 __device__ __forceinline__ void post_coefficients(const RowParams& p, uint32_t row, int j, float2& a, float2& b) {
     float2 g = make_float2(p.alpha, p.alpha);
     if (p.gate)
-        g = __fmul2_rn(g, __ldg(reinterpret_cast<const float2*>(p.gate + (row / p.gate_rows) * p.gate_stride + j)));
+        g = __fmul2_rn(g, ptx::ld_f2(p.gate + (row / p.gate_rows) * p.gate_stride + j));
     a = g;
     b = make_float2(0.0f, 0.0f);
-    if (p.post.weight) a = __fmul2_rn(g, __ldg(reinterpret_cast<const float2*>(p.post.weight + j)));
-    if (p.post.bias) b = __fmul2_rn(g, __ldg(reinterpret_cast<const float2*>(p.post.bias + j)));
+    if (p.post.weight) a = __fmul2_rn(g, ptx::ld_f2(p.post.weight + j));
+    if (p.post.bias) b = __fmul2_rn(g, ptx::ld_f2(p.post.bias + j));
 }
 
 // One row by a team of `nw` warps: warp j of it holds the segments j, j + nw,
@@ -77,9 +67,9 @@ __device__ __forceinline__ void one_row(const RowParams& p, uint32_t row, int j,
         const int c = (j + t * nw) * 32 + lane;
 #pragma unroll
         for (int q = 0; q < XQ; ++q)
-            xq[t][q] = c < nchunk ? ld_row(reinterpret_cast<const uint4*>(p.x) + (base + c) * XQ + q) : zero;
+            xq[t][q] = c < nchunk ? norm::ld_row(reinterpret_cast<const uint4*>(p.x) + (base + c) * XQ + q) : zero;
         if constexpr (HAS_Y)
-            yq[t] = c < nchunk ? ld_row(reinterpret_cast<const uint4*>(p.y) + base + c) : zero;
+            yq[t] = c < nchunk ? norm::ld_row(reinterpret_cast<const uint4*>(p.y) + base + c) : zero;
     }
     auto x_of = [&](int t, float2 (&v)[4]) {
         if constexpr (F32) norm::unpack(xq[t][0], xq[t][1], v);

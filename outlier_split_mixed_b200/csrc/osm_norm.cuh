@@ -14,6 +14,7 @@
 #include <cstdint>
 
 #include "osm_mx.cuh"
+#include "osm_ptx.cuh"
 
 namespace osm {
 namespace norm {
@@ -129,6 +130,16 @@ __device__ __forceinline__ float inverse_deviation(float m2, float inv_d, float 
     return rsqrtf(__fmaf_rn(m2, inv_d, eps));
 }
 
+// Loads of the rows: each byte is read once, so they bypass L1 (which serves
+// the coefficients).
+__device__ __forceinline__ uint4 ld_row(const uint4* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
 // (x - mean) * rstd on a pair.
 __device__ __forceinline__ float2 normalise(float2 x, float2 st) {
     return __fmul2_rn(__fadd2_rn(x, make_float2(-st.x, -st.x)), make_float2(st.y, st.y));
@@ -138,11 +149,11 @@ __device__ __forceinline__ float2 normalise(float2 x, float2 st) {
 // a = w (1 + scale), b = bias (1 + scale) + shift.
 __device__ __forceinline__ void coefficients(const Spec& s, int64_t mrow, int j, float2& a, float2& b) {
     a = make_float2(1.0f, 1.0f);
-    if (s.scale) a = __fadd2_rn(a, __ldg(reinterpret_cast<const float2*>(s.scale + mrow * s.mod_stride + j)));
+    if (s.scale) a = __fadd2_rn(a, ptx::ld_f2(s.scale + mrow * s.mod_stride + j));
     b = make_float2(0.0f, 0.0f);
-    if (s.bias) b = __fmul2_rn(a, __ldg(reinterpret_cast<const float2*>(s.bias + j)));
-    if (s.shift) b = __fadd2_rn(b, __ldg(reinterpret_cast<const float2*>(s.shift + mrow * s.mod_stride + j)));
-    if (s.weight) a = __fmul2_rn(a, __ldg(reinterpret_cast<const float2*>(s.weight + j)));
+    if (s.bias) b = __fmul2_rn(a, ptx::ld_f2(s.bias + j));
+    if (s.shift) b = __fadd2_rn(b, ptx::ld_f2(s.shift + mrow * s.mod_stride + j));
+    if (s.weight) a = __fmul2_rn(a, ptx::ld_f2(s.weight + j));
 }
 
 }  // namespace norm

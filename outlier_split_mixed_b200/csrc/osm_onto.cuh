@@ -16,6 +16,7 @@
 
 #include "osm_internal.h"
 #include "osm_mx.cuh"
+#include "osm_ptx.cuh"
 
 namespace osm {
 namespace onto {
@@ -88,9 +89,9 @@ struct Tile {
         __syncwarp();  // the last tile's readers are done
         const int64_t c = x0 + 4 * lane;
         if (c < p.N) {
-            if (p.bias) v.bias[lane] = __ldg(reinterpret_cast<const float4*>(p.bias + c));
+            if (p.bias) v.bias[lane] = ptx::ld_f4(p.bias + c);
             if (p.onto.gate && staged)
-                v.gate[lane] = __ldg(reinterpret_cast<const float4*>(p.onto.gate + group * p.onto.gate_stride + c));
+                v.gate[lane] = ptx::ld_f4(p.onto.gate + group * p.onto.gate_stride + c);
         }
         __syncwarp();
         // the residual words are read later: bring them into L2
@@ -154,8 +155,8 @@ struct Tile {
                     b = activate2(b, p.act);
                 }
                 if (p.onto.gate) {
-                    a = __fmul2_rn(a, staged ? vg[4 * i] : __ldg(reinterpret_cast<const float2*>(gate_a + 8 * i)));
-                    b = __fmul2_rn(b, staged ? vg[4 * i] : __ldg(reinterpret_cast<const float2*>(gate_b + 8 * i)));
+                    a = __fmul2_rn(a, staged ? vg[4 * i] : ptx::ld_f2(gate_a + 8 * i));
+                    b = __fmul2_rn(b, staged ? vg[4 * i] : ptx::ld_f2(gate_b + 8 * i));
                 }
                 if (p.onto.r) {
                     a = __fadd2_rn(from_word<F32>(w[2 * i]), a);

@@ -330,6 +330,21 @@ __device__ __forceinline__ void tma_store_2d_hint(const void* tmap, int32_t x, i
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" :::); }
 
+// Loads of operands that the previous kernel may have written (modulation and
+// gate rows from an embedding's projection). Not __ldg: such a kernel may still
+// be writing when this one starts, and a load of read-only memory has no order
+// with the wait. These stay behind it, and may pass stores to other addresses.
+__device__ __forceinline__ float2 ld_f2(const float* p) {
+    float2 v;
+    asm volatile("ld.global.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ float4 ld_f4(const float* p) {
+    float4 v;
+    asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+    return v;
+}
+
 // ---------------------------------------------------------------- clusters
 
 __device__ __forceinline__ uint32_t cluster_ctarank() {

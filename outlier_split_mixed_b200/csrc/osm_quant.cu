@@ -1285,7 +1285,7 @@ __global__ void __launch_bounds__(NormQuantShape<W, NS, TEAMS>::THREADS, MINB)
 #pragma unroll
                     for (int q = 0; q < XQ; ++q)
                         xq[r][t][q] = c < nchunk && r < rows
-                                          ? ldg_nc_v4(static_cast<const uint4*>(X) +
+                                          ? norm::ld_row(static_cast<const uint4*>(X) +
                                                       (static_cast<size_t>(row + r) * nchunk + c) * XQ + q)
                                           : make_uint4(0, 0, 0, 0);
             }

@@ -584,3 +584,54 @@ def test_two_streams_at_once():
     for i in range(2):
         for _, y in got[i]:
             same(y, want[i])
+
+
+@pytest.mark.parametrize("M, B", [(2, 2), (40, 1), (1200, 3)])
+def test_modulation_written_by_the_kernel_before(M, B):
+    """Modulation and gate rows come from linear_hp's call just before the norm and the products that read them, in one
+    buffer that the next step overwrites: each step gets the bits of a run that waits after every call."""
+    g = gen(M + B)
+    D, steps = 512, 12
+    embed = osm.HpLinear(rand(g, 256, 3 * D, dtype=BF, scale=0.05), rand(g, 3 * D, scale=0.1))
+    lin = osm.HpLinear(rand(g, D, D, dtype=BF, scale=0.05))
+    qlin = osm.QuantLinear(make_plan(g, D, D, 16), rand(g, D, D, dtype=BF, scale=0.05))
+    es = [rand(g, B, 256, dtype=BF) for _ in range(steps)]
+    xs = [rand(g, M, D, dtype=BF, scale=1.5) for _ in range(steps)]
+    mod, h, a = torch.empty(B, 3 * D, device="cuda"), torch.empty(M, D, dtype=BF, device="cuda"), qlin.plan.alloc_packed(M)
+    shift, scale, gate = mod[:, :D], mod[:, D:2 * D], mod[:, 2 * D:]
+    n = osm.Norm(scale=scale, shift=shift)
+
+    def step(i, out, wait):
+        embed.forward(es[i], out=mod)
+        wait()
+        osm.norm_modulate(xs[i], n, out=h)
+        wait()
+        lin.forward(h, gate=gate, residual=xs[i], out=out)
+        wait()
+        embed.forward(es[i - 1], out=mod)
+        wait()
+        osm.residual_norm(out, h, gate=gate, pre=n, out=out, h=h)
+        wait()
+        embed.forward(es[i], out=mod)
+        wait()
+        qlin.forward(out, norm=n, residual=out, gate=gate, out=out, act_buffers=a)
+        wait()
+
+    want = [torch.empty(M, D, dtype=BF, device="cuda") for _ in range(steps)]
+    for i in range(steps):
+        step(i, want[i], torch.cuda.synchronize)
+    got = [torch.zeros(M, D, dtype=BF, device="cuda") for _ in range(steps)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for i in range(steps):
+            step(i, got[i], lambda: None)
+    for _ in range(5):
+        graph.replay()
+        for i in range(steps):
+            same(got[i], want[i])
+            got[i].zero_()
+    for i in range(steps):
+        step(i, got[i], lambda: None)
+    for i in range(steps):
+        same(got[i], want[i])
+    assert embed.plan.status() == 0 and lin.plan.status() == 0 and qlin.plan.status() == 0
