@@ -38,15 +38,29 @@ struct RowParams {
 };
 
 // h = n a + b of the pre-norm, and (y or its norm) a + b of the gated sum:
-// alpha, gate and the post-norm's affine part in one pair.
-__device__ __forceinline__ void post_coefficients(const RowParams& p, uint32_t row, int j, float2& a, float2& b) {
-    float2 g = make_float2(p.alpha, p.alpha);
-    if (p.gate)
-        g = __fmul2_rn(g, ptx::ld_f2(p.gate + (row / p.gate_rows) * p.gate_stride + j));
-    a = g;
-    b = make_float2(0.0f, 0.0f);
-    if (p.post.weight) a = __fmul2_rn(g, ptx::ld_f2(p.post.weight + j));
-    if (p.post.bias) b = __fmul2_rn(g, ptx::ld_f2(p.post.bias + j));
+// alpha, gate and the post-norm's affine part in one pair; columns j .. j + 3.
+__device__ __forceinline__ void post_coefficients4(const RowParams& p, uint32_t row, int j, float2 (&a)[2],
+                                                   float2 (&b)[2]) {
+    const float2 alpha = make_float2(p.alpha, p.alpha);
+    float2 g[2] = {alpha, alpha};
+    if (p.gate) {
+        const float4 v = ptx::ld_f4(p.gate + (row / p.gate_rows) * p.gate_stride + j);
+        g[0] = __fmul2_rn(alpha, make_float2(v.x, v.y));
+        g[1] = __fmul2_rn(alpha, make_float2(v.z, v.w));
+    }
+    a[0] = g[0];
+    a[1] = g[1];
+    b[0] = b[1] = make_float2(0.0f, 0.0f);
+    if (p.post.weight) {
+        const float4 v = ptx::ld_f4(p.post.weight + j);
+        a[0] = __fmul2_rn(g[0], make_float2(v.x, v.y));
+        a[1] = __fmul2_rn(g[1], make_float2(v.z, v.w));
+    }
+    if (p.post.bias) {
+        const float4 v = ptx::ld_f4(p.post.bias + j);
+        b[0] = __fmul2_rn(g[0], make_float2(v.x, v.y));
+        b[1] = __fmul2_rn(g[1], make_float2(v.z, v.w));
+    }
 }
 
 // One row by a team of `nw` warps: warp j of it holds the segments j, j + nw,
@@ -196,17 +210,12 @@ __global__ void __launch_bounds__(32 * WARPS, MINB) rows_kernel(const __grid_con
             for (int i = threadIdx.x; i < ntab / 2 * nchunk; i += 32 * WARPS) {
                 const int k = i / nchunk, c = i - k * nchunk;  // k: table * 2 + half
                 const int col = c * norm::CHUNK + 4 * (k & 1);
-                float2 a0, a1, b0, b1;
-                if (HAS_Y && k < 2) {
-                    post_coefficients(p, first, col, a0, b0);
-                    post_coefficients(p, first, col + 2, a1, b1);
-                } else {
-                    norm::coefficients(p.pre, first / p.pre_rows, col, a0, b0);
-                    norm::coefficients(p.pre, first / p.pre_rows, col + 2, a1, b1);
-                }
+                float2 a[2], b[2];
+                if (HAS_Y && k < 2) post_coefficients4(p, first, col, a, b);
+                else norm::coefficients4(p.pre, first / p.pre_rows, col, a, b);
                 float4* at = table + ((k >> 1) * 4 + (k & 1)) * nchunk + c;
-                at[0] = make_float4(a0.x, a0.y, a1.x, a1.y);
-                at[2 * nchunk] = make_float4(b0.x, b0.y, b1.x, b1.y);
+                at[0] = make_float4(a[0].x, a[0].y, a[1].x, a[1].y);
+                at[2 * nchunk] = make_float4(b[0].x, b[0].y, b[1].x, b[1].y);
             }
             __syncthreads();
         }
@@ -237,9 +246,11 @@ __global__ void __launch_bounds__(512, MINB) row_kernel(const __grid_constant__ 
         const uint32_t r = static_cast<uint32_t>(row);
         auto coef = [&](int which, int c, float2 (&a)[4], float2 (&b)[4]) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (HAS_Y && which == 0) post_coefficients(p, r, c * norm::CHUNK + 2 * i, a[i], b[i]);
-                else norm::coefficients(p.pre, r / p.pre_rows, c * norm::CHUNK + 2 * i, a[i], b[i]);
+            for (int i = 0; i < 4; i += 2) {
+                float2 a2[2], b2[2];
+                if (HAS_Y && which == 0) post_coefficients4(p, r, c * norm::CHUNK + 2 * i, a2, b2);
+                else norm::coefficients4(p.pre, r / p.pre_rows, c * norm::CHUNK + 2 * i, a2, b2);
+                a[i] = a2[0], a[i + 1] = a2[1], b[i] = b2[0], b[i + 1] = b2[1];
             }
         };
         one_row<F32, HAS_Y, NS>(p, r, j, nw, lane, inv_d, total, coef);

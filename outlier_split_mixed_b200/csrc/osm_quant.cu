@@ -1214,7 +1214,10 @@ struct NormQuantShape {
     }
 };
 
-template <int MODE, bool F32, int W, int NS, int TEAMS, int MINB>
+// EACH: few tokens to a modulation row. The coefficients then come from global
+// memory for each row, where they are used; per token they are four times the bytes
+// of a BF16 row (4096 x 5120: 46 us, 4.9 TB/s; norm_modulate and quantize_act 49 + 15).
+template <int MODE, bool F32, bool EACH, int W, int NS, int TEAMS, int MINB>
 __global__ void __launch_bounds__(NormQuantShape<W, NS, TEAMS>::THREADS, MINB)
     norm_quantize_rows_kernel(QuantParams p, norm::Spec s, const void* X, uint32_t share, uint32_t tile_rows,
                               uint32_t tiles_per_run, uint32_t tiles) {
@@ -1257,20 +1260,19 @@ __global__ void __launch_bounds__(NormQuantShape<W, NS, TEAMS>::THREADS, MINB)
 
     uint32_t held = 0xffffffffu;
     for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const uint32_t run = tile / tiles_per_run, first = run * share;
+        const uint32_t run = EACH ? 0 : tile / tiles_per_run, first = run * share;
         const uint32_t row0 = first + (tile - run * tiles_per_run) * tile_rows;
-        const uint32_t end = min(min(row0 + tile_rows, first + share), static_cast<uint32_t>(p.M));
+        const uint32_t end = min(EACH ? row0 + tile_rows : min(row0 + tile_rows, first + share), static_cast<uint32_t>(p.M));
         if (held != run) {
             if (held != 0xffffffffu) __syncthreads();  // the rows of the last run are done
             held = run;
             const int64_t mrow = s.scale || s.shift ? first / s.mod_rows : 0;
-            for (int i = tid; i < 2 * nchunk; i += Shape::THREADS) {
+            for (int i = tid; !EACH && i < 2 * nchunk; i += Shape::THREADS) {
                 const int half = i >= nchunk, c = i - half * nchunk, col = c * norm::CHUNK + 4 * half;
-                float2 a0, a1, b0, b1;
-                norm::coefficients(s, mrow, col, a0, b0);
-                norm::coefficients(s, mrow, col + 2, a1, b1);
-                reinterpret_cast<float4*>(table)[half * nchunk + c] = make_float4(a0.x, a0.y, a1.x, a1.y);
-                reinterpret_cast<float4*>(table)[(2 + half) * nchunk + c] = make_float4(b0.x, b0.y, b1.x, b1.y);
+                float2 a[2], b[2];
+                norm::coefficients4(s, mrow, col, a, b);
+                reinterpret_cast<float4*>(table)[half * nchunk + c] = make_float4(a[0].x, a[0].y, a[1].x, a[1].y);
+                reinterpret_cast<float4*>(table)[(2 + half) * nchunk + c] = make_float4(b[0].x, b[0].y, b[1].x, b[1].y);
             }
             __syncthreads();
         }
@@ -1331,30 +1333,44 @@ __global__ void __launch_bounds__(NormQuantShape<W, NS, TEAMS>::THREADS, MINB)
                 const int c = (j + t * W) * 32 + lane;
                 if (c >= nchunk) continue;
                 const uint4* at = table + c;
-                const uint4 a0 = at[0], a1 = at[nchunk], b0 = at[2 * nchunk], b1 = at[3 * nchunk], s0 = at[4 * nchunk],
-                            s1 = at[5 * nchunk], r0 = at[6 * nchunk], r1 = at[7 * nchunk];
+                const uint4 s0 = at[4 * nchunk], s1 = at[5 * nchunk], r0 = at[6 * nchunk], r1 = at[7 * nchunk];
                 auto pair = [](uint32_t x, uint32_t y) { return make_float2(__uint_as_float(x), __uint_as_float(y)); };
-                const float2 ca[4] = {pair(a0.x, a0.y), pair(a0.z, a0.w), pair(a1.x, a1.y), pair(a1.z, a1.w)};
-                const float2 cb[4] = {pair(b0.x, b0.y), pair(b0.z, b0.w), pair(b1.x, b1.y), pair(b1.z, b1.w)};
                 const float2 cs[4] = {pair(s0.x, s0.y), pair(s0.z, s0.w), pair(s1.x, s1.y), pair(s1.z, s1.w)};
                 const uint32_t to[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
                 float2 x0[4], x1[4];
                 x_of(0, t, x0);
                 x_of(1, t, x1);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t w0 = norm_smooth2<false>(x0[i], st[0], ca[i], cb[i], cs[i], 0u);
-                    const uint32_t w1 = norm_smooth2<false>(x1[i], st[1], ca[i], cb[i], cs[i], 0u);
+                // columns 2i, 2i + 1 of both rows
+                auto put = [&](int i, float2 ca0, float2 cb0, float2 ca1, float2 cb1) {
+                    const uint32_t w0 = norm_smooth2<false>(x0[i], st[0], ca0, cb0, cs[i], 0u);
+                    const uint32_t w1 = norm_smooth2<false>(x1[i], st[1], ca1, cb1, cs[i], 0u);
                     uint32_t lo = __byte_perm(w0, w1, 0x5410), hi = __byte_perm(w0, w1, 0x7632);
                     if constexpr (HPF) {  // the slots of an FP16 outlier branch: the same products in binary16
-                        const uint32_t u0 = norm_smooth2<true>(x0[i], st[0], ca[i], cb[i], cs[i], 0xFFFFFFFFu);
-                        const uint32_t u1 = norm_smooth2<true>(x1[i], st[1], ca[i], cb[i], cs[i], 0xFFFFFFFFu);
+                        const uint32_t u0 = norm_smooth2<true>(x0[i], st[0], ca0, cb0, cs[i], 0xFFFFFFFFu);
+                        const uint32_t u1 = norm_smooth2<true>(x1[i], st[1], ca1, cb1, cs[i], 0xFFFFFFFFu);
                         const uint32_t slots = nb * IP_BLOCK;
                         if (to[2 * i] >= slots) lo = __byte_perm(u0, u1, 0x5410);
                         if (to[2 * i + 1] >= slots) hi = __byte_perm(u0, u1, 0x7632);
                     }
                     ptx::st_shared_u32(stage + to[2 * i], lo);
                     ptx::st_shared_u32(stage + to[2 * i + 1], hi);
+                };
+                if constexpr (EACH) {
+                    const int64_t m0 = row / share, m1 = (row + rows - 1) / share;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float2 a0[2], b0[2], a1[2], b1[2];
+                        norm::coefficients4(s, m0, c * norm::CHUNK + 4 * h, a0, b0);
+                        norm::coefficients4(s, m1, c * norm::CHUNK + 4 * h, a1, b1);
+                        put(2 * h, a0[0], b0[0], a1[0], b1[0]);
+                        put(2 * h + 1, a0[1], b0[1], a1[1], b1[1]);
+                    }
+                } else {
+                    const uint4 a0 = at[0], a1 = at[nchunk], b0 = at[2 * nchunk], b1 = at[3 * nchunk];
+                    const float2 ca[4] = {pair(a0.x, a0.y), pair(a0.z, a0.w), pair(a1.x, a1.y), pair(a1.z, a1.w)};
+                    const float2 cb[4] = {pair(b0.x, b0.y), pair(b0.z, b0.w), pair(b1.x, b1.y), pair(b1.z, b1.w)};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) put(i, ca[i], cb[i], ca[i], cb[i]);
                 }
             }
             team_sync();  // staged pair complete
@@ -1563,13 +1579,13 @@ static int launch_dependent(K kern, unsigned grid, unsigned threads, size_t smem
     return check_cuda(cudaLaunchKernelEx(&cfg, kern, args...), "norm_quantize_act launch");
 }
 
-template <bool F32, int W, int NS, int TEAMS, int MINB>
+template <bool F32, bool EACH, int W, int NS, int TEAMS, int MINB>
 static int launch_norm_quantize_rows(const QuantParams& p, int mode, const norm::Spec& s, const void* X, int64_t M,
                                      int64_t run, cudaStream_t st) {
     using Shape = NormQuantShape<W, NS, TEAMS>;
-    auto kern = mode == QA_NV ? norm_quantize_rows_kernel<QA_NV, F32, W, NS, TEAMS, MINB>
-                              : (mode == QA_MX_F16 ? norm_quantize_rows_kernel<QA_MX_F16, F32, W, NS, TEAMS, MINB>
-                                                   : norm_quantize_rows_kernel<QA_MX, F32, W, NS, TEAMS, MINB>);
+    auto kern = mode == QA_NV ? norm_quantize_rows_kernel<QA_NV, F32, EACH, W, NS, TEAMS, MINB>
+                              : (mode == QA_MX_F16 ? norm_quantize_rows_kernel<QA_MX_F16, F32, EACH, W, NS, TEAMS, MINB>
+                                                   : norm_quantize_rows_kernel<QA_MX, F32, EACH, W, NS, TEAMS, MINB>);
     const size_t smem = Shape::smem(p.K, p.Kbp >> 5, p.kp);
     int per_sm = 0, sms = 0;
     int rc = prepare_kernel(reinterpret_cast<const void*>(kern), Shape::THREADS, smem, &per_sm, &sms);
@@ -1577,9 +1593,10 @@ static int launch_norm_quantize_rows(const QuantParams& p, int mode, const norm:
     if (per_sm < 1) return fail(OSM_ERR_UNSUPPORTED, "norm_quantize_act: no CTA fits (K = %d)", p.K);
     // one tile per CTA: each run is cut into its part of them
     const int64_t ctas = static_cast<int64_t>(sms) * per_sm;
-    const int64_t cuts = ctas * run / M > 1 ? ctas * run / M : 1;
-    const int64_t tile_rows = ceil_div(run, cuts), per_run = ceil_div(run, tile_rows);
-    const int64_t tiles = ceil_div(M, run) * per_run;
+    const int64_t part = EACH ? M : run;
+    const int64_t cuts = ctas * part / M > 1 ? ctas * part / M : 1;
+    const int64_t tile_rows = ceil_div(part, cuts), per_run = ceil_div(part, tile_rows);
+    const int64_t tiles = ceil_div(M, part) * per_run;
     return launch_dependent(kern, static_cast<unsigned>(tiles < ctas ? tiles : ctas), Shape::THREADS, smem,
                             st, p, s, X, static_cast<uint32_t>(run), static_cast<uint32_t>(tile_rows),
                             static_cast<uint32_t>(per_run), static_cast<uint32_t>(tiles));
@@ -1595,15 +1612,23 @@ int launch_norm_quantize(const osm_plan* pl, const void* X, int x_dtype, int64_t
     const int nseg = static_cast<int>(ceil_div(pl->K, norm::SEG));
     const int64_t run = spec->scale || spec->shift ? (M < spec->mod_rows ? M : spec->mod_rows) : M;
     // Teams of warps (norm_quantize_rows_kernel) while a row pair fits their
-    // registers, unless the tables would have to be laid out anew for every few
-    // rows of many (5120 columns in us, one row per CTA against teams: 1 row 17.5
-    // and 11.5, 1000 rows 29.2 and 16.8, 4000 rows in runs of 16 71 and 41).
-    if (pl->K <= 5120 && (run >= 8 || M <= 148)) {
-        if (pl->K <= 1024)
-            return f32 ? launch_norm_quantize_rows<true, 2, 2, 8, 2>(p, mode, s, X, M, run, st)
-                       : launch_norm_quantize_rows<false, 2, 2, 8, 2>(p, mode, s, X, M, run, st);
-        return f32 ? launch_norm_quantize_rows<true, 4, 5, 4, 1>(p, mode, s, X, M, run, st)
-                   : launch_norm_quantize_rows<false, 4, 5, 6, 1>(p, mode, s, X, M, run, st);
+    // registers (one row of 5120 columns: 11.5 us, by a CTA 17.5). Of many rows, those
+    // in short runs take their coefficients from global memory instead of laying
+    // out a table for each run (4096 x 5120 BF16, us, table and global: runs of 8 41
+    // and 36, of 16 36 and 36, of 32 31 and 36; runs of 1 46, by a CTA per row 79).
+    // Fewer teams then, for the registers of the second row's coefficients (6, 5, 4
+    // teams: 63, 47, 46).
+    if (pl->K <= 5120) {
+        const bool each = run < 16 && M > 148, narrow = pl->K <= 1024;
+        auto rows = [&](auto e) {
+            constexpr bool E = decltype(e)::value;
+            if (narrow)
+                return f32 ? launch_norm_quantize_rows<true, E, 2, 2, 8, E ? 1 : 2>(p, mode, s, X, M, run, st)
+                           : launch_norm_quantize_rows<false, E, 2, 2, 8, 2>(p, mode, s, X, M, run, st);
+            return f32 ? launch_norm_quantize_rows<true, E, 4, 5, 4, 1>(p, mode, s, X, M, run, st)
+                       : launch_norm_quantize_rows<false, E, 4, 5, E ? 4 : 6, 1>(p, mode, s, X, M, run, st);
+        };
+        return each ? rows(std::true_type{}) : rows(std::false_type{});
     }
     const size_t smem = ((2 * nseg * 4 + 15) & ~15) + qa_row_stride(static_cast<int>(pl->Kbp / 32), static_cast<int>(pl->kp));
     auto pick = [&](auto f) {

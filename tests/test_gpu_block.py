@@ -252,6 +252,22 @@ def test_norm_quantize_act_writes_what_the_two_calls_write(fmt, dtype, K, k):
         assert plan.status() == 0
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("K", [512, 2048, 5120])
+@pytest.mark.parametrize("M, run", [(149, 1), (301, 2), (1000, 3), (1283, 7), (1283, 15), (1283, 16), (148, 3)])
+def test_norm_quantize_act_of_short_runs(dtype, K, M, run):
+    g = gen(K + M + run)
+    plan = make_plan(g, K, 32, 16)
+    x, e = rand(g, M, K, dtype=dtype, scale=1.5, shift=0.3), rand(g, -(-M // run), 2 * K + 8, scale=0.3)
+    n = osm.Norm(weight=rand(g, K), bias=rand(g, K), scale=e[:, :K], shift=e[:, K:2 * K], mod_rows=run)
+    want = plan.alloc_packed(M)
+    osm.quantize_act(plan, osm.norm_modulate(x, n), *want)
+    got = guarded(plan, M)
+    osm.norm_quantize_act(plan, x, n, *[v for _, v, _ in got])
+    for (b, v, size), w in zip(got, want):
+        assert torch.equal(b[:size], w.reshape(-1).view(torch.uint8)) and bool((b[size:] == 0xA5).all())
+
+
 # ------------------------------------------------------------ dual_gemm_residual
 
 def operands(g, plan, M, N):
