@@ -149,10 +149,13 @@ int osm_dual_gemm_residual(const osm_plan* p, const uint8_t* a_codes, const uint
                 "dual_gemm_residual: outlier operands null or misaligned");
     OSM_TRY(check_device());
     const Onto onto = onto_of(R, gate, gate_rows, gate_stride, M);
+    // gate rows shorter than the 32 rows of an epilogue warp are not staged (4096 x
+    // 5120 x 5120 onto BF16, a gate row per token: 89 us, through the staging kernel 111;
+    // FP32 rows leave no registers for the form that loads several at once)
+    const int epi = r_dtype == OSM_DT_F32 ? EPI_ONTO_F32 : (gate && gate_rows < 32 && M > gate_rows ? EPI_ONTO_EACH : EPI_ONTO_BF16);
     return guarded([&] {
         return launch_dual_gemm(p, a_codes, a_scales, a_hp, M, w_codes, w_scales, w_hp, bias,
-                                r_dtype == OSM_DT_F32 ? EPI_ONTO_F32 : EPI_ONTO_BF16, Y, nullptr, nullptr, nullptr,
-                                nullptr, static_cast<cudaStream_t>(stream), &onto);
+                                epi, Y, nullptr, nullptr, nullptr, nullptr, static_cast<cudaStream_t>(stream), &onto);
     });
 }
 

@@ -81,7 +81,7 @@ static_assert(LAUNCH_REGS * 3 <= 512 && CTRL_REGS % 8 == 0 && EPI_REGS % 8 == 0,
 // allocation; the FFN requantisation and the residual sum (which holds the
 // residual's words beside the accumulators) need more than LAUNCH_REGS.
 __host__ __device__ constexpr bool uses_register_split(int epi) {
-    return epi == OSM_EPI_GELU_REQUANT || epi == EPI_ONTO_BF16 || epi == EPI_ONTO_F32;
+    return epi == OSM_EPI_GELU_REQUANT || epi >= EPI_ONTO_BF16;
 }
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t SF_COL0 = 256;       // scale factors live after the accumulator
@@ -543,8 +543,8 @@ __device__ __forceinline__ void epilogue_role(const GemmParams& p, Smem<NV>& S, 
     const int half = warp >> 2;  // columns [128*half, 128*half + 128) of the tile
     const uint32_t acc_empty_leader = ptx::mapa(ptx::smem_u32(&S.acc_empty), 0);
     uint32_t acc_phase = 0;
-    constexpr bool ONTO = EPI == EPI_ONTO_BF16 || EPI == EPI_ONTO_F32;
-    onto::Tile<EPI == EPI_ONTO_F32> end;
+    constexpr bool ONTO = EPI >= EPI_ONTO_BF16;
+    onto::Tile<EPI == EPI_ONTO_F32, EPI == EPI_ONTO_EACH> end;
     onto::Vectors* vectors = nullptr;
     if constexpr (ONTO) vectors = &epilogue_vectors<EPI>(warp);
     for (int tile = pair; tile < tiles; tile += npairs) {
@@ -831,6 +831,9 @@ int launch_dual_gemm(const osm_plan* pl, const uint8_t* a_codes, const uint8_t* 
         case EPI_ONTO_BF16:
             kernel = nv ? dual_gemm_kernel<EPI_ONTO_BF16, true> : dual_gemm_kernel<EPI_ONTO_BF16, false>;
             break;
+        case EPI_ONTO_EACH:
+            kernel = nv ? dual_gemm_kernel<EPI_ONTO_EACH, true> : dual_gemm_kernel<EPI_ONTO_EACH, false>;
+            break;
         case EPI_ONTO_F32:
             kernel = nv ? dual_gemm_kernel<EPI_ONTO_F32, true> : dual_gemm_kernel<EPI_ONTO_F32, false>;
             break;
@@ -838,7 +841,7 @@ int launch_dual_gemm(const osm_plan* pl, const uint8_t* a_codes, const uint8_t* 
     }
 
     // co-resident clusters of two CTAs, queried once per device and epilogue
-    static LaunchInfo info[64][12];
+    static LaunchInfo info[64][14];
     static std::mutex mu;
     int dev = 0;
     if ((rc = check_cuda(cudaGetDevice(&dev), "cudaGetDevice"))) return rc;

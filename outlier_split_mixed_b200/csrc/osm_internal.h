@@ -84,7 +84,8 @@ struct Onto {
     int64_t gate_rows, gate_stride;
 };
 // Epilogues of the dual GEMM beyond osm_epi: onto a residual stream.
-constexpr int EPI_ONTO_BF16 = 4, EPI_ONTO_F32 = 5;
+// EPI_ONTO_EACH: onto BF16 with a gate row for every few tokens.
+constexpr int EPI_ONTO_BF16 = 4, EPI_ONTO_F32 = 5, EPI_ONTO_EACH = 6;
 
 // A two-dimensional tensor map (rows of `inner` elements) for tiled TMA copies.
 int make_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t rows,

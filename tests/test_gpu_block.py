@@ -307,6 +307,21 @@ def test_dual_gemm_residual(fmt, dtype, M, K, N, k):
         assert plan.status() == 0
 
 
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("M, share", [(2, 1), (33, 31), (259, 3), (700, 16), (700, 31), (700, 32), (700, 33)])
+def test_dual_gemm_residual_short_gate_rows(fmt, dtype, M, share):
+    g = gen(M + share)
+    plan = make_plan(g, 256, 416, 16, fmt)
+    a, w = operands(g, plan, M, 416)
+    r, gates, bias = rand(g, M, 416, dtype=dtype, scale=2.0), rand(g, -(-M // share), 424), rand(g, 416)
+    y = torch.empty(M, 416, device="cuda")
+    osm.dual_gemm(plan, *a, M, *w, y, bias=bias, epi=osm.EPI_F32)
+    want = (r.float() + y * gates[torch.arange(M, device="cuda") // share, :416]).to(dtype)
+    same(osm.dual_gemm_residual(plan, *a, M, *w, r, bias=bias, gate=gates[:, :416], gate_rows=share), want)
+    assert plan.status() == 0
+
+
 # ------------------------------------------------------------ linear_hp
 
 def act64(y, act):
