@@ -344,11 +344,14 @@ int launch_single(const RowParams& p, cudaStream_t st) {
 
 template <bool F32, bool HAS_Y>
 int launch_width(const RowParams& p, cudaStream_t st) {
-    // Tiles pay from two rows per SM on, while a run's coefficients serve a few
-    // rows (5120 columns in us, a CTA per row against tiles: 100 rows 7.7 and 8.8,
-    // 300 rows 11.1 and 9.3, 3000 rows 38.7 and 19.8). The coefficients of 14336
-    // columns (both tables) fill shared memory.
-    const bool tiles = p.M >= 2 * 148 && p.share >= 8 && p.D <= 14336;
+    // Tiles pay once the rows are more than one round of CTAs with a row each, of
+    // up to 16 warps by the row's segments and 32 warps per SM, while a run's
+    // coefficients serve a few rows (us, a CTA per row against tiles: 5120 columns,
+    // 296 rows 3.8 and 4.4, 400 rows 6.0 and 4.8, 3000 rows 21.7 and 14.8; 1024
+    // columns, 1000 rows 3.2 and 3.4, 3000 rows 6.0 and 5.5). The coefficients of
+    // 14336 columns (both tables) fill shared memory.
+    const int64_t round = 148 * 32 / std::min<int64_t>(16, ceil_div(p.D, norm::SEG));
+    const bool tiles = p.M > round && p.share >= 8 && p.D <= 14336;
     if (!tiles) {
         if (p.D <= 8192) return launch_single<F32, HAS_Y, 2, 2>(p, st);
         if (p.D <= 16384) return launch_single<F32, HAS_Y, 4, F32 ? 1 : 2>(p, st);
