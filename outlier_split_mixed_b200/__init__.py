@@ -13,6 +13,7 @@ outlier branch is BF16 (Eq. (3)).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -683,13 +684,19 @@ class Norm:
         return -2  # no device: tensors of the host are refused
 
 
+def _allocating_for(stream, device):
+    """A context in which tensors are allocated for the stream that uses them: freed inside the call that uses them there,
+    their memory goes to that stream's next allocation, which waits for that use; the current stream's would not."""
+    if stream is None:
+        return contextlib.nullcontext()
+    import torch
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream)
+
+
 def _new(shape, dtype, like, stream):
     """An output tensor, allocated for the stream that will write it."""
     import torch
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    s = torch.cuda.ExternalStream(stream, device=like.device) if isinstance(stream, int) else stream
-    with torch.cuda.stream(s):
+    with _allocating_for(stream, like.device):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
@@ -850,10 +857,10 @@ def calibrate(X_batches, W, alpha: float, k: int, stream=None):
 
 class QuantLinear:
     """A packed layer: plan + resident packed weights. `forward(X)` runs
-    quantize_act and dual_gemm on the current stream; with `norm` the rows
-    are normalised on the way (norm_quantize_act), with `residual` the
-    product is gated and added to it and has its type, whatever epi says
-    (dual_gemm_residual)."""
+    quantize_act and dual_gemm on `stream` (default: the current one); with
+    `norm` the rows are normalised on the way (norm_quantize_act), with
+    `residual` the product is gated and added to it and has its type, whatever
+    epi says (dual_gemm_residual)."""
 
     def __init__(self, plan: Plan, W, bias=None, device="cuda"):
         self.plan = plan
@@ -867,7 +874,10 @@ class QuantLinear:
         M = X.shape[0]
         if residual is None and gate is not None:
             raise ValueError("gate goes with residual")
-        a = act_buffers if act_buffers is not None else self.plan.alloc_packed(M, X.device)
+        a = act_buffers
+        if a is None:
+            with _allocating_for(stream, X.device):
+                a = self.plan.alloc_packed(M, X.device)
         if norm is not None:
             norm_quantize_act(self.plan, X, norm, *a, stream=stream)
         else:
@@ -876,8 +886,7 @@ class QuantLinear:
             return dual_gemm_residual(self.plan, *a, M, self.w_codes, self.w_scales, self.w_hp, residual, out=out,
                                       bias=self.bias, gate=gate, gate_rows=gate_rows, stream=stream)
         if out is None:
-            out = torch.empty((M, self.plan.N), dtype=torch.float32 if epi == EPI_F32 else torch.bfloat16,
-                              device=X.device)
+            out = _new((M, self.plan.N), torch.float32 if epi == EPI_F32 else torch.bfloat16, X, stream)
         dual_gemm(self.plan, *a, M, self.w_codes, self.w_scales, self.w_hp, out, bias=self.bias, epi=epi,
                   stream=stream)
         return out

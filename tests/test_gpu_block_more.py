@@ -1,0 +1,48 @@
+"""Further cases of the operators around the layers on the GPU: layers on
+several streams at once."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import outlier_split_mixed_b200 as osm  # noqa: E402
+from test_gpu_block import BF, gen, make_plan, rand, same  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    osm.lib()
+
+
+@pytest.mark.parametrize("as_address", [False, True])
+def test_quantised_layers_on_two_streams_at_once(as_address):
+    # each call packs its activations into buffers of its own, which are free again when it returns
+    g = gen(81)
+    K, N, M = 2048, 512, 3000
+    plan = make_plan(g, K, N, 64)
+    lin = osm.QuantLinear(plan, rand(g, K, N, dtype=BF, scale=0.03))
+    n = osm.Norm(scale=rand(g, K, scale=0.3), shift=rand(g, K))
+    xs = [rand(g, M, K, dtype=BF) for _ in range(2)]
+    rs = [rand(g, M, N) for _ in range(2)]
+    calls = [dict(), dict(epi=osm.EPI_BF16), dict(norm=n), dict(norm=n, residual=True)]
+
+    def call(i, kw, stream):
+        kw = dict(kw, residual=rs[i]) if "residual" in kw else kw
+        return lin.forward(xs[i], stream=stream, **kw)
+
+    want = [[call(i, kw, None) for kw in calls] for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(10):
+        for j, kw in enumerate(calls):
+            for i in range(2):
+                got[i].append((j, call(i, kw, streams[i].cuda_stream if as_address else streams[i])))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for j, y in got[i]:
+            same(y, want[i][j])
+    assert plan.status() == 0
