@@ -121,6 +121,15 @@ def _check(rc: int):
         raise OsmError(rc, last_error())
 
 
+def _allocating_for(stream, device):
+    """A context in which tensors are allocated for the stream that uses them: freed inside the call that uses them there,
+    their memory goes to that stream's next allocation, which waits for that use; the current stream's would not."""
+    if stream is None:
+        return contextlib.nullcontext()
+    import torch
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream)
+
+
 _raw_stream = None  # torch's current stream of a device, as its address
 
 
@@ -319,10 +328,11 @@ def error_norms(Y, Yref, stream=None):
     import torch
     if Y.shape != Yref.shape:
         raise ValueError("Y and Yref differ in shape")
-    out = torch.zeros(2, dtype=torch.float64, device=Y.device)
-    _check(lib().osm_error_norms(_ptr(Y, "Y", (torch.float32,)), _ptr(Yref, "Yref", (torch.float32,)), Y.numel(),
-                                 _ptr(out, "out", (torch.float64,)), _stream(stream)))
-    e, n = out.cpu().tolist()
+    with _allocating_for(stream, Y.device):
+        out = torch.zeros(2, dtype=torch.float64, device=Y.device)
+        _check(lib().osm_error_norms(_ptr(Y, "Y", (torch.float32,)), _ptr(Yref, "Yref", (torch.float32,)), Y.numel(),
+                                     _ptr(out, "out", (torch.float64,)), _stream(stream)))
+        e, n = out.cpu().tolist()
     return e, n
 
 
@@ -330,7 +340,8 @@ def gelu_f32(x, y=None, stream=None):
     """The FFN epilogues' FP32 GELU routine element-wise (osm_gelu_f32)."""
     import torch
     if y is None:
-        y = torch.empty_like(x)
+        with _allocating_for(stream, x.device):
+            y = torch.empty_like(x)
     if x.dtype != torch.float32 or y.dtype != torch.float32 or x.numel() != y.numel():
         raise ValueError("x and y must be float32 tensors of one size")
     _check(lib().osm_gelu_f32(_ptr(x, "x"), _ptr(y, "y"), x.numel(), _stream(stream)))
@@ -684,15 +695,6 @@ class Norm:
         return -2  # no device: tensors of the host are refused
 
 
-def _allocating_for(stream, device):
-    """A context in which tensors are allocated for the stream that uses them: freed inside the call that uses them there,
-    their memory goes to that stream's next allocation, which waits for that use; the current stream's would not."""
-    if stream is None:
-        return contextlib.nullcontext()
-    import torch
-    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream)
-
-
 def _new(shape, dtype, like, stream):
     """An output tensor, allocated for the stream that will write it."""
     import torch
@@ -845,12 +847,14 @@ def calibrate(X_batches, W, alpha: float, k: int, stream=None):
     then Eq. (2)/(4) on the host: returns (s, inv_s, O, amax, wmax)."""
     import torch
     K = W.shape[0]
-    amax = torch.zeros(K, dtype=torch.float32, device=W.device)
-    wmax = torch.empty(K, dtype=torch.float32, device=W.device)
+    with _allocating_for(stream, W.device):
+        amax = torch.zeros(K, dtype=torch.float32, device=W.device)
+        wmax = torch.empty(K, dtype=torch.float32, device=W.device)
     for X in X_batches:
         act_amax_accumulate(X, amax, stream)
     weight_amax(W, wmax, stream)
-    a, w = amax.cpu().numpy(), wmax.cpu().numpy()
+    with _allocating_for(stream, W.device):  # the copies to the host wait for that stream
+        a, w = amax.cpu().numpy(), wmax.cpu().numpy()
     s, inv_s, O = calibrate_finalize(a, w, alpha, k)
     return s, inv_s, O, a, w
 

@@ -46,3 +46,25 @@ def test_quantised_layers_on_two_streams_at_once(as_address):
         for j, y in got[i]:
             same(y, want[i][j])
     assert plan.status() == 0
+
+
+def test_calibration_on_another_stream():
+    # the statistics are complete when they are read, whatever the current stream does
+    g = gen(82)
+    x, w = rand(g, 20000, 4096, dtype=BF), rand(g, 4096, 2048, dtype=BF)
+    want = osm.calibrate([x, 2 * x], w, 0.5, 32)
+    y = rand(g, 5000, 4096)
+    norms, act = osm.error_norms(y, 2 * y), osm.gelu_f32(y)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    twice, double = 2 * x, 2 * y
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = osm.calibrate([x, twice], w, 0.5, 32, stream=side)
+        assert all((a == b).all() for a, b in zip(got, want))
+        # CTAs (148 x 8 at most) add their FP64 sums in any order: none is negative, so each order is within
+        # 1184 roundings of 2^-53 of the exact sum and any two orders within twice that
+        assert all(abs(a - b) <= 2 * 1184 * 2.0 ** -53 * b for a, b in zip(osm.error_norms(y, double, stream=side), norms))
+        z = osm.gelu_f32(y, stream=side)
+        side.synchronize()
+        same(z, act)

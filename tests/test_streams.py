@@ -59,3 +59,39 @@ def test_a_layers_buffers_belong_to_the_stream_of_its_kernels(allocations, norm,
     allocations.clear()
     layer().forward(x, norm=norm, residual=r)
     assert set(allocations) == {"current"}
+
+
+@pytest.mark.parametrize("stream", ["side", None])
+def test_statistics_are_cleared_and_read_on_the_stream_of_their_kernels(allocations, monkeypatch, stream):
+    cleared, read = [], []
+    zeros, cpu = torch.zeros, torch.Tensor.cpu
+    on = lambda: (torch.empty(1), allocations.pop())[1]  # noqa: E731
+
+    def recorded_zeros(*args, **kw):
+        cleared.append(on())
+        return zeros(*args, **kw)
+
+    def recorded_cpu(t):
+        read.append(on())
+        return cpu(t)
+
+    class Library:
+        osm_error_norms = staticmethod(lambda *a: 0)
+        osm_gelu_f32 = staticmethod(lambda *a: 0)
+
+    for name in ("act_amax_accumulate", "weight_amax"):
+        monkeypatch.setattr(osm, name, lambda *a: None)
+    monkeypatch.setattr(osm, "calibrate_finalize", lambda *a: (None, None, None))
+    monkeypatch.setattr(osm, "_ptr", lambda *a: None)
+    monkeypatch.setattr(osm, "_stream", lambda s: s)
+    monkeypatch.setattr(osm, "lib", Library)
+    monkeypatch.setattr(torch, "zeros", recorded_zeros)
+    monkeypatch.setattr(torch.Tensor, "cpu", recorded_cpu)
+    x, w = torch.ones(4, 32), torch.ones(32, 8)
+    osm.calibrate([x], w, 0.5, 4, stream=stream)
+    osm.error_norms(x, x, stream=stream)
+    where = stream or "current"
+    assert cleared == [where] * 2 and read == [where] * 3 and allocations == [where]
+    monkeypatch.setattr(torch, "empty_like", lambda t: (allocations.append(on()), t.clone())[1])
+    osm.gelu_f32(x, stream=stream)
+    assert allocations[-1] == where
