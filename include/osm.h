@@ -494,8 +494,10 @@ OSM_API int osm_dual_gemm_residual(const osm_plan* plan, const uint8_t* a_codes,
  *   y = act(X W + bias),  Y = T([R +] [gate[t / gate_rows] *] y)
  * X [M][K] BF16; FP32 accumulation; act one of OSM_ACT_*; bias float[N] or
  * NULL; gate as above or NULL; R [M][N] of Y's type T (y_dtype) or NULL. Y
- * may be R. 1 <= M < 2^31. The plan's outlier branch must be BF16. A pipeline
- * wait that exceeds the plan's wait limit sets OSM_STATUS_TIMEOUT. */
+ * may be R. 1 <= M < 2^31. The plan's outlier branch must be BF16, and g_w = 0
+ * in an NVFP4 plan (its slots hold w 2^-g_w; with no bulk channels
+ * osm_nvfp4_plan_exponents gives 0). A pipeline wait that exceeds the plan's
+ * wait limit sets OSM_STATUS_TIMEOUT. */
 #define OSM_ACT_NONE 0
 #define OSM_ACT_GELU 1 /* the tanh form of the FFN epilogues */
 #define OSM_ACT_SILU 2 /* x / (1 + exp(-x)) */

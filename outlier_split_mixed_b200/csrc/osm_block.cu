@@ -167,6 +167,9 @@ int osm_linear_hp(const osm_plan* p, const uint16_t* X, int64_t M, const uint16_
     OSM_REQUIRE(p->k == p->K && p->unit_s, "linear_hp: needs a plan with k = K and s = 1 (k=%lld, K=%lld)",
                 (long long)p->k, (long long)p->K);
     OSM_REQUIRE(!p->hp_fp16, "linear_hp: needs the BF16 outlier branch");
+    // an NVFP4 plan's packed slots are w 2^-g_w, and X here is not scaled
+    OSM_REQUIRE(p->fmt == OSM_FMT_MXFP4 || p->g_w == 0, "linear_hp: the weights of an NVFP4 plan must be unscaled (g_w = %d)",
+                p->g_w);
     OSM_REQUIRE(M >= 1 && M <= (int64_t(1) << 31) - 1, "linear_hp: need 1 <= M < 2^31");
     OSM_REQUIRE(act == OSM_ACT_NONE || act == OSM_ACT_GELU || act == OSM_ACT_SILU, "linear_hp: unknown activation %d",
                 act);

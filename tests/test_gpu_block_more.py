@@ -1,5 +1,6 @@
 """Further cases of the operators around the layers on the GPU: layers on
-several streams at once."""
+several streams at once, plans of other formats."""
+import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -68,3 +69,22 @@ def test_calibration_on_another_stream():
         z = osm.gelu_f32(y, stream=side)
         side.synchronize()
         same(z, act)
+
+
+def test_linear_hp_of_nvfp4_plans():
+    # packed slots hold w 2^-g_w and X is not scaled: with g_w = 0 it is the product, anything else is refused
+    g = gen(83)
+    ones, every = np.ones(64, np.float32), np.arange(64, dtype=np.int32)
+    x, W = rand(g, 40, 64, dtype=BF), rand(g, 64, 96, dtype=BF, scale=0.1)
+    want = osm.HpLinear(W).forward(x)
+    for g_act, g_w in ((-6, 0), (0, 0), (-6, -8), (0, 3)):
+        plan = osm.Plan(64, 96, 64, ones, every, fmt=osm.FMT_NVFP4, g_act=g_act, g_w=g_w)
+        w = plan.alloc_packed(96)
+        osm.pack_weights(plan, W, *w)
+        if g_w == 0:
+            same(osm.linear_hp(plan, x, w[2]), want)
+            assert plan.status() == 0
+        else:
+            with pytest.raises(osm.OsmError, match="g_w") as e:
+                osm.linear_hp(plan, x, w[2])
+            assert e.value.code == osm.ERR_INVALID_ARG
