@@ -241,8 +241,11 @@ OSM_API int osm_nvfp4_plan_exponents(const float* amax_host, const float* wmax_h
  * group than its copies deliver, so every wait on a row group runs out after
  * the wait limit: the kernel sets OSM_STATUS_TIMEOUT, waits (bounded) for
  * its copies and returns; its outputs are incomplete. Nothing faults: the
- * copies themselves complete. 0 restores normal operation. */
+ * copies themselves complete. OSM_DEBUG_STARVE_LINEAR: the same for
+ * osm_linear_hp, whose CTAs expect 16 bytes more for their first K-step.
+ * 0 restores normal operation. */
 #define OSM_DEBUG_STARVE_QUANTIZE 1u
+#define OSM_DEBUG_STARVE_LINEAR   2u
 OSM_API int osm_plan_set_debug(osm_plan* plan, uint32_t flags);
 
 /* Channel order in which a previous layer must produce this plan's input

@@ -29,7 +29,7 @@ STATUS_TIMEOUT = 1
 HP_BF16, HP_FP16 = 0, 1
 FMT_MXFP4, FMT_NVFP4 = 0, 1
 STATUS_NONFINITE = 2
-DEBUG_STARVE_QUANTIZE = 1
+DEBUG_STARVE_QUANTIZE, DEBUG_STARVE_LINEAR = 1, 2
 WSCALE_1x32, WSCALE_TILE32x32, WSCALE_STRIP128x1 = 0, 1, 2
 EPI_F32, EPI_BF16, EPI_GELU_REQUANT, EPI_GELU_BF16 = 0, 1, 2, 3
 DT_BF16, DT_F32 = 0, 1

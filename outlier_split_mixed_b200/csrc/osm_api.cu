@@ -374,7 +374,7 @@ int osm_nvfp4_plan_exponents(const float* amax, const float* wmax, const float* 
 int osm_plan_set_debug(osm_plan* p, uint32_t flags) {
     g_err[0] = 0;
     OSM_REQUIRE(p, "plan_set_debug: plan is NULL");
-    OSM_REQUIRE((flags & ~static_cast<uint32_t>(OSM_DEBUG_STARVE_QUANTIZE)) == 0, "plan_set_debug: unknown flag");
+    OSM_REQUIRE((flags & ~(OSM_DEBUG_STARVE_QUANTIZE | OSM_DEBUG_STARVE_LINEAR)) == 0, "plan_set_debug: unknown flag");
     p->debug_flags = flags;
     return OSM_OK;
 }

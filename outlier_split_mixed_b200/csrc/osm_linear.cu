@@ -51,6 +51,7 @@ struct LinearParams {
     onto::Params end;    // sizes and the end of the product
     uint32_t* status;
     uint64_t wait_limit_ns;
+    uint32_t starve;     // bytes that a CTA's first K-step waits for in vain (0 outside of failure tests)
     int ksteps;
     int num_m, num_n, group_m;  // pair_kernel: tiles and raster
 };
@@ -172,7 +173,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PK_THREADS, 1)
         ptx::setmaxnreg_dec<PK_CTRL_REGS>();
         if (warp == PK_PRODUCER && ptx::elect_one()) {
             int stage = 0, last_stage = -1;
-            uint32_t phase = 0, last_phase = 0;
+            uint32_t phase = 0, last_phase = 0, starve = p.starve;
             bool ok = true;
             for (int tile = pair; tile < tiles && ok; tile += npairs) {
                 int m, n;
@@ -185,7 +186,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PK_THREADS, 1)
                         break;
                     }
                     const uint32_t fb = ptx::mapa(ptx::smem_u32(&S.full[stage]), 0);
-                    if (leader) ptx::mbar_arrive_expect_tx(ptx::smem_u32(&S.full[stage]), 4u * TILE);
+                    if (leader) ptx::mbar_arrive_expect_tx(ptx::smem_u32(&S.full[stage]), 4u * TILE + starve);
+                    starve = 0;
                     ptx::tma_load_2d_pair(ptx::smem_u32(S.a[stage]), &p.tm_x, ks * KSTEP, arow, fb);
                     ptx::tma_load_2d_pair(ptx::smem_u32(S.b[stage]), &p.tm_w, ks * KSTEP, brow, fb);
                     last_stage = stage;
@@ -402,7 +404,7 @@ __global__ void __launch_bounds__(SK_THREADS) skinny_kernel(const __grid_constan
     if (warp == 4) {
         if (ptx::elect_one()) {
             int stage = 0, issued = 0;
-            uint32_t phase = 0;
+            uint32_t phase = 0, starve = p.starve;
             bool ok = true;
             for (int ks = k0; ks < k1; ++ks, ++issued) {
                 if (!ptx::mbar_wait_bounded(ptx::smem_u32(&S.empty[stage]), phase ^ 1u, p.wait_limit_ns, abort)) {
@@ -410,7 +412,8 @@ __global__ void __launch_bounds__(SK_THREADS) skinny_kernel(const __grid_constan
                     break;
                 }
                 const uint32_t fb = ptx::smem_u32(&S.full[stage]);
-                ptx::mbar_arrive_expect_tx(fb, slot_bytes);
+                ptx::mbar_arrive_expect_tx(fb, slot_bytes + starve);
+                starve = 0;
                 ptx::tma_load_2d(ring_u32 + stage * slot_bytes, &p.tm_w, ks * KSTEP, n0, fb);
                 ptx::tma_load_2d(ring_u32 + stage * slot_bytes + TILE, &p.tm_x, ks * KSTEP, m0, fb);
                 if (++stage == stages) { stage = 0; phase ^= 1u; }
@@ -754,6 +757,7 @@ int launch_linear_hp(const osm_plan* pl, const uint16_t* X, int64_t M, const uin
     p.end = onto::Params{M, pl->N, bias, Y, onto, 1.0f, act};
     p.status = pl->d_status;
     p.wait_limit_ns = pl->wait_limit_ns;
+    p.starve = (pl->debug_flags & OSM_DEBUG_STARVE_LINEAR) ? 16u : 0u;
     p.ksteps = static_cast<int>(pl->kp / KSTEP);
     const bool f32 = y_dtype == OSM_DT_F32;
     int dev = 0;

@@ -1,12 +1,13 @@
 """Further cases of the operators around the layers on the GPU: layers on
-several streams at once, plans of other formats."""
+several streams at once, plans of other formats, waits that run
+out."""
 import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
 
 import outlier_split_mixed_b200 as osm  # noqa: E402
-from test_gpu_block import BF, gen, make_plan, rand, same  # noqa: E402
+from test_gpu_block import BF, F32, gen, make_plan, operands, rand, same  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -88,3 +89,50 @@ def test_linear_hp_of_nvfp4_plans():
             with pytest.raises(osm.OsmError, match="g_w") as e:
                 osm.linear_hp(plan, x, w[2])
             assert e.value.code == osm.ERR_INVALID_ARG
+
+
+# Few tokens with and without K splits, and CTA pairs (every call above 4096 tokens; 2000 by the estimate of both times).
+STARVED = [(1, 128, 512), (1, 4096, 128), (48, 512, 256), (128, 128, 512), (100, 4096, 256), (2000, 4096, 2560),
+           (4352, 512, 512)]
+
+
+@pytest.mark.parametrize("M, K, N", STARVED)
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_linear_hp_starved_of_its_copies_reports_it(M, K, N, dtype):
+    # the first K-step of every CTA expects bytes that no copy brings: its wait runs out after 1 ms, the status says so,
+    # and the next call gets the same bits as before
+    g = gen(84)
+    lin = osm.HpLinear(rand(g, K, N, dtype=BF, scale=0.02))
+    x = rand(g, M, K, dtype=BF)
+    want = lin.forward(x, dtype=dtype)
+    assert lin.plan.status() == 0
+    lin.plan.set_wait_limit(1_000_000)
+    lin.plan.set_debug(osm.DEBUG_STARVE_LINEAR)
+    lin.forward(x, dtype=dtype)
+    assert lin.plan.status() == osm.STATUS_TIMEOUT
+    lin.plan.set_debug(0)
+    lin.plan.set_wait_limit(2_000_000_000)
+    same(lin.forward(x, dtype=dtype), want)
+    assert lin.plan.status() == 0
+    with pytest.raises(osm.OsmError):
+        lin.plan.set_debug(4)
+
+
+@pytest.mark.parametrize("dtype, share", [(BF, 1024), (F32, 1024), (BF, 1)])
+def test_dual_gemm_residual_reports_a_wait_that_runs_out(dtype, share):
+    # a limit of 1 us is far below the time of a tile's MMAs and of an epilogue's end (the three epilogues: BF16, FP32, a
+    # gate row per token onto BF16)
+    g = gen(85)
+    M, K, N = 1024, 5120, 13824
+    plan = make_plan(g, K, N, 128)
+    a, w = operands(g, plan, M, N)
+    r, gate = rand(g, M, N, dtype=dtype), rand(g, M // share, N)
+    call = lambda: osm.dual_gemm_residual(plan, *a, M, *w, r, gate=gate, gate_rows=share)  # noqa: E731
+    want = call()
+    assert plan.status() == 0
+    plan.set_wait_limit(1000)
+    call()
+    assert plan.status() == osm.STATUS_TIMEOUT
+    plan.set_wait_limit(2_000_000_000)
+    same(call(), want)
+    assert plan.status() == 0
