@@ -863,8 +863,9 @@ class QuantLinear:
     """A packed layer: plan + resident packed weights. `forward(X)` runs
     quantize_act and dual_gemm on `stream` (default: the current one); with
     `norm` the rows are normalised on the way (norm_quantize_act), with
-    `residual` the product is gated and added to it and has its type, whatever
-    epi says (dual_gemm_residual)."""
+    `residual` the product is gated and added to it and has its type: EPI_F32
+    and EPI_BF16 are the same there, an epi with GELU is refused
+    (dual_gemm_residual)."""
 
     def __init__(self, plan: Plan, W, bias=None, device="cuda"):
         self.plan = plan
@@ -878,6 +879,8 @@ class QuantLinear:
         M = X.shape[0]
         if residual is None and gate is not None:
             raise ValueError("gate goes with residual")
+        if residual is not None and epi in (EPI_GELU_BF16, EPI_GELU_REQUANT):
+            raise ValueError("the product onto a residual takes no activation: epi with GELU does not go with residual")
         a = act_buffers
         if a is None:
             with _allocating_for(stream, X.device):
