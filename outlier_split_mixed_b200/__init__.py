@@ -864,7 +864,7 @@ class QuantLinear:
     quantize_act and dual_gemm on `stream` (default: the current one); with
     `norm` the rows are normalised on the way (norm_quantize_act), with
     `residual` the product is gated and added to it and has its type: EPI_F32
-    and EPI_BF16 are the same there, an epi with GELU is refused
+    and EPI_BF16 are the same there, every other epi is refused
     (dual_gemm_residual)."""
 
     def __init__(self, plan: Plan, W, bias=None, device="cuda"):
@@ -879,7 +879,7 @@ class QuantLinear:
         M = X.shape[0]
         if residual is None and gate is not None:
             raise ValueError("gate goes with residual")
-        if residual is not None and epi in (EPI_GELU_BF16, EPI_GELU_REQUANT):
+        if residual is not None and epi not in (EPI_F32, EPI_BF16):
             raise ValueError("the product onto a residual takes no activation: epi with GELU does not go with residual")
         a = act_buffers
         if a is None:
