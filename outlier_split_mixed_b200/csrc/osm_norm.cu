@@ -100,7 +100,7 @@ __device__ __forceinline__ void one_row(const RowParams& p, uint32_t row, int j,
                 get(t, v);
                 part[t] = norm::chunk_sum(v);
             }
-            mean = __fmul_rn(total(part), inv_d);
+            mean = norm::mean_of(total(part), static_cast<float>(p.D), inv_d);
         }
 #pragma unroll
         for (int t = 0; t < NS; ++t) {

@@ -1123,7 +1123,10 @@ __global__ void __launch_bounds__(QA_THREADS) norm_quantize_kernel(QuantParams p
             return norm::join_total<256>(at, nseg, lane);
         };
         float mean = 0.0f;
-        if (center) mean = __fmul_rn(total(part, [](const float2 (&v)[4]) { return norm::chunk_sum(v); }), inv_d);
+        if (center) {
+            const float sum = total(part, [](const float2 (&v)[4]) { return norm::chunk_sum(v); });
+            mean = norm::mean_of(sum, static_cast<float>(p.K), inv_d);
+        }
         const float m2 = total(part + nseg, [&](const float2 (&v)[4]) { return norm::chunk_m2(v, mean); });
         const float2 st[1] = {make_float2(mean, norm::inverse_deviation(m2, inv_d, s.eps))};
         const int64_t mrow = s.scale || s.shift ? t / s.mod_rows : 0;
@@ -1313,8 +1316,9 @@ __global__ void __launch_bounds__(NormQuantShape<W, NS, TEAMS>::THREADS, MINB)
                         x_of(r, t, v);
                         value[r][t] = norm::chunk_sum(v);
                     }
-                mean = totals(part);
-                mean = __fmul2_rn(mean, make_float2(inv_d, inv_d));
+                const float2 sum = totals(part);
+                const float d = static_cast<float>(p.K);
+                mean = make_float2(norm::mean_of(sum.x, d, inv_d), norm::mean_of(sum.y, d, inv_d));
             }
 #pragma unroll
             for (int r = 0; r < 2; ++r)

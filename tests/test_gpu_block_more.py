@@ -136,3 +136,35 @@ def test_dual_gemm_residual_reports_a_wait_that_runs_out(dtype, share):
     plan.set_wait_limit(2_000_000_000)
     same(call(), want)
     assert plan.status() == 0
+
+
+def constants(M, D, dtype):
+    """Rows of one value each: the 128 BF16 mantissas by powers of two from 2^-9 on, both signs."""
+    r = torch.arange(M, device="cuda")
+    c = (128 + r % 128) * 2.0 ** (r // 128 % 16 - 9) * (1 - 2 * (r // 7 % 2))
+    return c.to(dtype)[:, None].expand(M, D).contiguous()
+
+
+# Widths whose reciprocal in FP32, times the exact sum, misses most constants: a CTA per row and tiles of rows
+@pytest.mark.parametrize("D, M", [(480, 128), (480, 2560), (960, 1280), (2016, 640), (3840, 256), (3840, 384), (6080, 384),
+                                  (14344, 128)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_constant_rows_have_no_deviation(D, M, dtype):
+    # the sum of D equal BF16 values is exact in FP32 in any order, and so is its quotient by D: N(x) = 0 to the bit
+    g = gen(86)
+    x, shift = constants(M, D, dtype), rand(g, D)
+    n = osm.Norm(weight=rand(g, D), scale=rand(g, D, scale=0.3), shift=shift)
+    want = shift.to(BF).expand(M, D)
+    h = osm.norm_modulate(x, n)
+    same(h, want)
+    r, bias = rand(g, M, D, dtype=dtype), rand(g, D)
+    out, h = osm.residual_norm(r, x.to(BF), post=osm.Norm(weight=rand(g, D), bias=bias), pre=n)
+    same(out, (r.float() + bias).to(dtype))
+    plan = make_plan(g, D // 32 * 32, 32, 16)
+    xq = x[:, :plan.K].contiguous()
+    nq = osm.Norm(shift=shift[:plan.K].clone())
+    a, b = plan.alloc_packed(M), plan.alloc_packed(M)
+    osm.norm_quantize_act(plan, xq, nq, *a)
+    osm.quantize_act(plan, shift[:plan.K].to(BF).expand(M, plan.K).contiguous(), *b)
+    for got, ref in zip(a, b):
+        same(got, ref)
