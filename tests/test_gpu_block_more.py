@@ -1,13 +1,14 @@
 """Further cases of the operators around the layers on the GPU: layers on
 several streams at once, plans of other formats, waits that run
-out."""
+out, rows in tiles at every width. Tolerances as in test_gpu_block.py."""
 import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
 
 import outlier_split_mixed_b200 as osm  # noqa: E402
-from test_gpu_block import BF, F32, gen, make_plan, operands, rand, same  # noqa: E402
+from test_gpu_block import (BF, F32, HALF, U, gen, make_norm, make_plan, modulation, norm64, operands, rand,  # noqa: E402
+                            same, within)
 
 pytestmark = pytest.mark.gpu
 
@@ -168,3 +169,71 @@ def test_constant_rows_have_no_deviation(D, M, dtype):
     osm.quantize_act(plan, shift[:plan.K].to(BF).expand(M, plan.K).contiguous(), *b)
     for got, ref in zip(a, b):
         same(got, ref)
+
+
+# Just over the rows from which each width is cut into tiles (148 SMs x 32 warps over the warps of a row), as far as the
+# widest; with one run of rows and with three
+@pytest.mark.parametrize("M, D", [(6000, 64), (5000, 256), (2500, 504), (1300, 1016), (1300, 1024), (600, 2040), (600, 2048),
+                                  (400, 5128), (400, 8184), (400, 8192), (400, 13816), (400, 14336)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("mode", ["one", "batch"])
+@pytest.mark.parametrize("post", [None, osm.NORM_RMS])
+def test_rows_in_tiles(M, D, dtype, mode, post):
+    g = gen(87)
+    x, y = rand(g, M, D, dtype=dtype, scale=2.0, shift=0.7), rand(g, M, D, dtype=BF, shift=0.2)
+    n, tokens = make_norm(g, M, D, osm.NORM_LAYER, True, mode)
+    href, he = norm64(x, n, tokens)
+    within(osm.norm_modulate(x, n), href, he + 2.0 ** -8 * (href.abs() + he) + 1e-37)
+    p = None if post is None else make_norm(g, M, D, post, True, "none")[0]
+    (gate,), share = modulation(g, M, D, mode, 1)
+    out, h = osm.residual_norm(x, y, gate=gate, gate_rows=share, alpha=0.5, post=p, pre=n)
+    t, e = (y.double(), torch.zeros(M, D, device="cuda").double()) if p is None else norm64(y, p, M)
+    gd = 0.5 * gate.double()[torch.arange(M, device="cuda") // share]
+    ref = x.double() + gd * t
+    e = e * gd.abs() + 4 * U * (x.double().abs() + 2 * (gd * t).abs())
+    within(out, ref, e + HALF[dtype] * (ref.abs() + e))
+    href, he = norm64(out, n, tokens)
+    within(h, href, he + 2.0 ** -8 * (href.abs() + he) + 1e-37)
+    same(h, osm.norm_modulate(out, n))
+    alone, none = osm.residual_norm(x, y, gate=gate, gate_rows=share, alpha=0.5, post=p)
+    assert none is None
+    same(alone, out)
+    # in place, with rows behind the last that stay
+    xx, yy = torch.cat([x, x[:3]]), torch.cat([y, y[:3]])
+    osm.residual_norm(xx[:M], yy[:M], gate=gate, gate_rows=share, alpha=0.5, post=p, pre=n, out=xx[:M], h=yy[:M])
+    same(xx[:M], out)
+    same(yy[:M], h)
+    same(xx[M:], x[:3])
+    same(yy[M:], y[:3])
+
+
+def scale_bytes(buf, rows, nblocks, at):
+    """E8M0 bytes of the rows `at`, from the layout's definition: 512-byte atoms of 128 rows x 4 blocks, atoms of one row
+    group beside one another, row r and block b at 16 (r % 32) + 4 (r % 128 // 32) + b % 4."""
+    r, b = at[:, None], torch.arange(nblocks, device=buf.device)[None]
+    return buf[((r // 128) * (nblocks // 4) + b // 4) * 512 + r % 32 * 16 + r % 128 // 32 * 4 + b % 4]
+
+
+def test_norm_quantize_act_scales_past_32_bit_offsets():
+    free, _ = torch.cuda.mem_get_info()
+    if free < 40 << 30:
+        pytest.skip("needs 40 GiB of free device memory")
+    M, K = 900_003, 5120
+    plan = make_plan(gen(88), K, 32, 128)
+    base = rand(gen(89), 4099, K, dtype=BF)
+    x = torch.empty(M, K, dtype=BF, device="cuda")
+    for i in range(0, M, 4099):
+        n = min(4099, M - i)
+        x[i:i + n] = base[:n] * (1 + i % 7)
+    a = plan.alloc_packed(M)
+    norm = osm.Norm(osm.NORM_RMS, shift=rand(gen(90), K))
+    osm.norm_quantize_act(plan, x, norm, *a)
+    at = torch.tensor([0, 1, 127, 128, M // 2, 838_860, 838_861, M - 130, M - 2, M - 1], device="cuda")
+    few = plan.alloc_packed(at.numel())
+    osm.norm_quantize_act(plan, x[at], norm, *few)
+    every = torch.arange(at.numel(), device="cuda")
+    same(scale_bytes(a[1], M, plan.Kbp // 32, at), scale_bytes(few[1], at.numel(), plan.Kbp // 32, every))
+    # the rows that pad the last group of 128 have scale 0
+    pad = torch.arange(M, (M + 127) // 128 * 128, device="cuda")
+    assert bool((scale_bytes(a[1], M, plan.Kbp // 32, pad) == 0).all())
+    assert plan.status() == 0
