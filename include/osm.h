@@ -430,7 +430,9 @@ OSM_API int osm_ffn_block_host(const osm_plan* up, const osm_plan* down, const u
 
 /* N(x) = (x - mean) / sqrt(var + eps), var = mean((x - mean)^2) over the row,
  * or x / sqrt(mean(x^2) + eps). Statistics are FP32, the variance formed from
- * deviations (never as a difference of sums). */
+ * deviations (never as a difference of sums): a constant BF16 row has N = 0
+ * exactly. A finite row whose squares add up beyond FP32's range gives N = 0,
+ * one whose sum does NaN. */
 #define OSM_NORM_LAYER 0
 #define OSM_NORM_RMS   1
 
@@ -474,7 +476,11 @@ OSM_API int osm_residual_norm(const void* R, int r_dtype, const uint16_t* Y, int
                               float alpha, const osm_norm_spec* pre, void* R_out, uint16_t* H, void* stream);
 
 /* osm_norm_modulate followed by osm_quantize_act in one pass: writes the
- * same packed operands (bit for bit), without H in memory. X [M][plan->K]. */
+ * same packed operands (bit for bit), without H in memory. X [M][plan->K].
+ * Faster than the two calls for K <= 5120 (32760 x 5120 BF16: 154 against 205
+ * us); above that each CTA works on one row at a time and the two calls, with
+ * 2 M K bytes for H, are faster (32760 x 5152: 518 against 272 us, x 13824: 1082
+ * against 636). */
 OSM_API int osm_norm_quantize_act(const osm_plan* plan, const void* X, int x_dtype, int64_t M,
                                   const osm_norm_spec* norm, uint8_t* a_codes, uint8_t* a_scales, uint16_t* a_hp,
                                   void* stream);

@@ -14,8 +14,11 @@
 // What bounds them, measured on one B200 (back to back, power not capped): pair_kernel
 // the tensor pipe -- BF16 4096 x 5120 x 5120 in 149 us (1440 TFLOP/s), 32760
 // gated rows onto BF16 in 1141-1180 (1455-1505; the pipe 86 % active);
-// skinny_kernel the weights -- one token, 5120 x 5120, in 13.4 us (3.9 TB/s with
-// 4 us of start and end), 512 tokens in 33, where 1024 take pair_kernel 48.
+// skinny_kernel the weights -- one token, 5120 x 5120, in 14.2 us where the
+// weights come from HBM (3.7 TB/s with 4 us of start and end) and 11.3 where they
+// stayed in L2, 512 tokens in 33-35, where 1024 take pair_kernel 49. FP32 results
+// cost more: 4096 tokens 219 us where BF16 ones take 169 (both power capped), for
+// the sums of chunks and an end that runs under no other tile.
 // 256 x 256 tiles are the largest of which tensor memory holds two accumulators.
 // Every wait is bounded by %globaltimer; one that runs out sets the plan's
 // status word and the CTA returns after its copies and MMAs have finished.
@@ -673,7 +676,9 @@ struct SkinnyShape {
 
 // Time estimates in microseconds, fitted to sweeps on one B200 (K, N = 5120 x
 // 5120, 1504 x 4128, 5120 x 1024, 512 x 13824, 1 to 1536 tokens; within about a
-// tenth of the measured times). A launch of skinny_kernel costs 3.6, a CTA alone on
+// tenth of the measured times of plain products). Activation, gate and residual
+// are not in them: 1001 x 1504 x 4128 FP32 is estimated at 19.8, the plain product
+// takes 18.8, with GELU 20.5 (22.7 with inputs that change), with gate and residual 22. A launch of skinny_kernel costs 3.6, a CTA alone on
 // its SM takes a K-step of nt tokens in max(0.165, 0.115 + 0.00103 nt) (FP32, with
 // its chunks: max(0.22, 0.13 + 0.00103 nt)) and its tile's end in 0.03 a token; two on an SM take 0.86 of twice the steps and 0.042 a
 // token. Joining split sums costs 1.6, and the weights come at 6.2 TB/s.

@@ -4,11 +4,20 @@
 // (tcgen05.ld 16x256b: thread t has rows t / 4 and t / 4 + 8 and, of each
 // 8-column block j, columns 2 (t % 4) and the next in registers 4j .. 4j + 3).
 //
-// Nothing of the store loop waits on global memory: the residual words of a
-// slab are in registers before its accumulator (those of a tile's first slab
-// are loaded while the MMAs still run, those of the second as the first one's
-// are used up), bias and gate are in shared memory. Loaded in the store loop
-// instead they doubled dual_gemm's time at 4096 x 5120 x 5120 (104 -> 201 us).
+// Where a warp's 32 rows share a gate row (or there is none), nothing of the
+// store loop waits on global memory: the residual words of a slab are in
+// registers before its accumulator, those of the second slab loaded as the
+// first one's are used up, and bias and gate are in shared memory. The first
+// slab's words are loaded while the tile's MMAs still run, except by
+// pair_kernel<true> (osm_linear.cu), whose registers are full of sums until
+// then. Loaded in the store loop instead they doubled dual_gemm's time at
+// 4096 x 5120 x 5120 (104 -> 201 us).
+// Where the 32 rows have several gate rows, the store loop loads them from
+// global memory: four blocks' at a time in the EACH form, which dual_gemm onto
+// BF16 takes for gate rows of fewer than 32 tokens, one at a time in the
+// others (4096 x 5120 x 5120, a gate row per token against one for all:
+// dual_gemm BF16 95 and 71 us, FP32 123 and 84; linear_hp, which has no EACH
+// form, BF16 197 and 181, FP32 318 and 272).
 #pragma once
 
 #include <cstdint>

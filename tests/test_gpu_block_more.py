@@ -171,6 +171,22 @@ def test_constant_rows_have_no_deviation(D, M, dtype):
         same(got, ref)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("M, D", [(3, 512), (5, 5120), (400, 5120), (2, 20480)])
+def test_rows_beyond_the_range_of_their_statistics(M, D, dtype):
+    g = gen(91)
+    shift = rand(g, D)
+    n = osm.Norm(shift=shift)
+    x = rand(g, M, D, dtype=dtype)
+    want = osm.norm_modulate(x, n)
+    x[0] = rand(g, D, scale=1e19, dtype=dtype)  # squares of 1e38, hundreds of them: the sum of squares is infinite
+    x[1] = 3e38                                 # the sum itself is
+    h = osm.norm_modulate(x, n)
+    same(h[0], shift.to(BF))
+    assert bool(torch.isnan(h[1]).all())
+    same(h[2:], want[2:])
+
+
 # Just over the rows from which each width is cut into tiles (148 SMs x 32 warps over the warps of a row), as far as the
 # widest; with one run of rows and with three
 @pytest.mark.parametrize("M, D", [(6000, 64), (5000, 256), (2500, 504), (1300, 1016), (1300, 1024), (600, 2040), (600, 2048),
