@@ -253,3 +253,28 @@ def test_norm_quantize_act_scales_past_32_bit_offsets():
     pad = torch.arange(M, (M + 127) // 128 * 128, device="cuda")
     assert bool((scale_bytes(a[1], M, plan.Kbp // 32, pad) == 0).all())
     assert plan.status() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("M, K, N", [(300, 512, 1024), (8000, 5120, 64), (700, 5152, 64)])
+def test_normed_products_repeat_their_bits(M, K, N, dtype):
+    # nothing waits between the passes, and every second one is followed by another layer's on the same stream
+    g = gen(92)
+    lins = [osm.QuantLinear(make_plan(g, K, N, 64), rand(g, K, N, dtype=BF, scale=0.02)) for _ in range(2)]
+    xs = [rand(g, M, K, dtype=dtype, scale=1.5, shift=0.3) for _ in range(2)]
+    ns = [osm.Norm(scale=rand(g, K, scale=0.3), shift=rand(g, K)) for _ in range(2)]
+    acts = [lin.plan.alloc_packed(M) for lin in lins]
+    call = lambda i: lins[i].forward(xs[i], epi=osm.EPI_BF16, norm=ns[i], act_buffers=acts[i])  # noqa: E731
+    want = call(0)
+    packed = [t.clone() for t in acts[0]]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(50):
+        got.append(call(0))
+        if i % 2:
+            call(1)
+    for y in got:
+        same(y, want)
+    for a, p in zip(acts[0], packed):
+        same(a, p)
+    assert lins[0].plan.status() == 0
